@@ -1,4 +1,5 @@
-"""GB300 MoE expert-parallel layout / dispatch / combine.
+"""GB300 MoE expert-parallel layout / dispatch / combine, and the router and
+experts around them.
 
 A thin ctypes binding over the C ABI of libmoe_ep.so (include/moe_ep.h).  The
 functions carry the C names and only marshal arguments: they check dtypes and
@@ -28,6 +29,8 @@ MOE_LAYOUT_FORM_NONE, MOE_LAYOUT_FORM_SINGLE, MOE_LAYOUT_FORM_CLUSTER, \
 MOE_SYNC_WORD, MOE_SYNC_SENTINEL, MOE_SYNC_BATCH, MOE_SYNC_BARRIER = range(4)
 MOE_EP_TO_EXPERT, MOE_EP_TO_SOURCE = 0, 1
 MOE_MAX_EXPERTS = 1024
+MOE_W_BF16, MOE_W_E4M3 = 0, 1
+MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_PAIRS, MOE_MAX_TOPK = 64, 512, 32
 
 # Every symbol the header declares, with its ctypes signature.
 _P, _I, _SZ, _U32P = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
@@ -58,6 +61,16 @@ SIGNATURES = {
     "moe_dispatch_quant_coalesced": ([_I, _I, _I, _P, _P, _I, _P, _P, _U32P, _P], ctypes.c_int),
     "moe_combine_coalesced": ([_I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _I, _U32P, _P],
                               ctypes.c_int),
+    "moe_route": ([_I, _I, _I, _I, _I, _P, ctypes.c_int64, _I, _P, _P, _P], ctypes.c_int),
+    "moe_route_backward": ([_I, _I, _I, _P, _P, _P, _P, _I, _U32P, _P], ctypes.c_int),
+    "moe_expert_gemm": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _U32P, _P],
+                        ctypes.c_int),
+    "moe_expert_swiglu": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _U32P, _P],
+                          ctypes.c_int),
+    "moe_expert_wgrad": ([_I, _I, _I, _I, _P, _P, _P, _P, _U32P, _P], ctypes.c_int),
+    "moe_layer_few_workspace_bytes": ([_I, _I, _I, _I], ctypes.c_size_t),
+    "moe_layer_few": ([_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P, _SZ,
+                       _U32P, _P], ctypes.c_int),
     "moe_dispatch_combine_flagged": ([_I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P,
                                       ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int64, _U32P,
                                       _P], ctypes.c_int),
@@ -571,6 +584,8 @@ __all__ = [
     "moe_combine_coalesced",
     "moe_dispatch_combine_flagged", "moe_ep_reorder", "moe_layout_last_form",
     "moe_e4m3_encode_bits", "moe_ep_reorder_rows", "LIB_PATH",
+    "Routing", "moe_route", "moe_route_backward", "moe_expert_gemm", "moe_expert_swiglu",
+    "moe_expert_wgrad", "moe_layer_few", "moe_layer_few_workspace_bytes", "MoELayer",
     "SIGNATURES",
 ]
 
@@ -628,3 +643,8 @@ def moe_ep_reorder_rows(src: torch.Tensor, recv_counts: torch.Tensor, *, to_sour
                                     MOE_EP_TO_EXPERT, _ptr(local_expert_offsets),
                                     _ptr(err_word), _stream(stream)), "moe_ep_reorder_rows")
     return out
+
+
+from .experts import (MoELayer, Routing, moe_expert_gemm, moe_expert_swiglu,  # noqa: E402
+                      moe_expert_wgrad, moe_layer_few, moe_layer_few_workspace_bytes, moe_route,
+                      moe_route_backward)

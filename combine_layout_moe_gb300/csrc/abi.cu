@@ -409,6 +409,146 @@ moe_status moe_ep_reorder_rows(int W, int El, int row_bytes, const int32_t *recv
                                             err_word, stream));
 }
 
+moe_status moe_route(int T, int E, int k, int groups, int topk_groups, const void *logits,
+                     int64_t logits_stride, int logits_dtype, int32_t *topk_idx, float *topk_w,
+                     cudaStream_t stream)
+{
+    if (!pairs_ok(T, k) || E < 1 || groups < 1 || E % groups != 0 || topk_groups < 1 ||
+        topk_groups > groups || k > E / groups * topk_groups || logits_stride < E)
+        return MOE_ERR_INVALID_ARG;
+    if (logits_dtype != MOE_OUT_BF16 && logits_dtype != MOE_OUT_F32)
+        return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || groups > 32)
+        return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!logits || !topk_idx || !topk_w))
+        return MOE_ERR_INVALID_ARG;
+    const bool f32 = logits_dtype == MOE_OUT_F32;
+    if (!aligned(logits, f32 ? 4 : 2) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_route(T, E, k, groups, topk_groups, logits, logits_stride, f32,
+                                       topk_idx, topk_w, stream));
+}
+
+moe_status moe_route_backward(int T, int E, int k, const int32_t *topk_idx, const float *topk_w,
+                              const float *dw, void *dlogits, int dlogits_dtype,
+                              uint32_t *err_word, cudaStream_t stream)
+{
+    if (!pairs_ok(T, k) || E < 1 || k > E)
+        return MOE_ERR_INVALID_ARG;
+    if (dlogits_dtype != MOE_OUT_BF16 && dlogits_dtype != MOE_OUT_F32)
+        return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK)
+        return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!topk_idx || !topk_w || !dw || !dlogits))
+        return MOE_ERR_INVALID_ARG;
+    const bool f32 = dlogits_dtype == MOE_OUT_F32;
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(dw, 4) ||
+        !aligned(dlogits, f32 ? 4 : 2) || !aligned(err_word, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_route_backward(T, E, k, topk_idx, topk_w, dw, dlogits, f32,
+                                                err_word, stream));
+}
+
+moe_status moe_expert_gemm(int N, int K, int M, int E, const uint8_t *a_q, const float *a_scales,
+                           const int32_t *expert_offsets, const uint8_t *w_q,
+                           const float *w_scales, int transpose_w, void *out, int out_dtype,
+                           uint32_t *err_word, cudaStream_t stream)
+{
+    if (N < 0 || K < 128 || K % 128 != 0 || M < 16 || M % 16 != 0 || E < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (out_dtype != MOE_OUT_BF16 && out_dtype != MOE_OUT_F32)
+        return MOE_ERR_INVALID_ARG;
+    if (transpose_w != 0 && transpose_w != 1)
+        return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS)
+        return MOE_ERR_UNSUPPORTED;
+    if (N > 0 && (!a_q || !a_scales || !expert_offsets || !w_q || !w_scales || !out))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(a_q, 16) || !aligned(a_scales, 16) || !aligned(w_q, 16) ||
+        !aligned(w_scales, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4) ||
+        !aligned(err_word, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_expert_gemm(N, K, M, E, a_q, a_scales, expert_offsets, w_q,
+                                             w_scales, transpose_w != 0, out,
+                                             out_dtype == MOE_OUT_F32, err_word, stream));
+}
+
+moe_status moe_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q,
+                             const float *a_scales, const int32_t *expert_offsets,
+                             const uint8_t *w_q, const float *w_scales, uint8_t *h_q,
+                             float *h_scales, uint32_t *err_word, cudaStream_t stream)
+{
+    if (N < 0 || K < 128 || K % 128 != 0 || I < 128 || I % 128 != 0 || I > (1 << 30) || E < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS)
+        return MOE_ERR_UNSUPPORTED;
+    if (N > 0 && (!a_q || !a_scales || !expert_offsets || !w_q || !w_scales || !h_q || !h_scales))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(a_q, 16) || !aligned(a_scales, 16) || !aligned(w_q, 16) ||
+        !aligned(w_scales, 16) || !aligned(h_q, 16) || !aligned(h_scales, 16) ||
+        !aligned(expert_offsets, 4) || !aligned(err_word, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_expert_swiglu(N, K, I, E, a_q, a_scales, expert_offsets, w_q,
+                                               w_scales, h_q, h_scales, err_word, stream));
+}
+
+moe_status moe_expert_wgrad(int N, int M, int K, int E, const void *dy, const void *x,
+                            const int32_t *expert_offsets, float *dw, uint32_t *err_word,
+                            cudaStream_t stream)
+{
+    if (N < 0 || M < 8 || M % 8 != 0 || K < 8 || K % 8 != 0 || E < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS)
+        return MOE_ERR_UNSUPPORTED;
+    if (!expert_offsets || !dw || (N > 0 && (!dy || !x)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(expert_offsets, 4) ||
+        !aligned(err_word, 4))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_expert_wgrad(N, M, K, E, dy, x, expert_offsets, dw, err_word,
+                                              stream));
+}
+
+size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I)
+{
+    if (T < 0 || T > MOE_FEW_MAX_TOKENS || k < 1 || k > MOE_MAX_TOPK ||
+        T * k > MOE_FEW_MAX_PAIRS || H < 8 || H % 8 != 0 || I < 8 || I % 8 != 0 || I > (1 << 30))
+        return 0;
+    return moe::layer_few_workspace_bytes(T, k, H, I);
+}
+
+moe_status moe_layer_few(int T, int k, int H, int I, int E, const void *x,
+                         const int32_t *topk_idx, const float *topk_w, const void *w13,
+                         const float *w13_scales, const void *w2, const float *w2_scales,
+                         int weight_dtype, void *out, int out_dtype, void *workspace,
+                         size_t workspace_bytes, uint32_t *err_word, cudaStream_t stream)
+{
+    if (weight_dtype != MOE_W_BF16 && weight_dtype != MOE_W_E4M3)
+        return MOE_ERR_INVALID_ARG;
+    const bool fp8 = weight_dtype == MOE_W_E4M3;
+    const int step = fp8 ? 128 : 8;
+    if (T < 0 || k < 1 || E < 1 || H < step || H % step != 0 || I < step || I % step != 0 ||
+        I > (1 << 30))
+        return MOE_ERR_INVALID_ARG;
+    if (out_dtype != MOE_OUT_BF16 && out_dtype != MOE_OUT_F32)
+        return MOE_ERR_INVALID_ARG;
+    if (T > MOE_FEW_MAX_TOKENS || k > MOE_MAX_TOPK || T * k > MOE_FEW_MAX_PAIRS ||
+        E > MOE_MAX_EXPERTS)
+        return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!x || !topk_idx || !topk_w || !w13 || !w2 || !out || !workspace ||
+                  (fp8 && (!w13_scales || !w2_scales))))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || !aligned(w13_scales, 16) || !aligned(w2_scales, 16) ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(err_word, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe::layer_few_workspace_bytes(T, k, H, I))
+        return MOE_ERR_INVALID_ARG;
+    return from_cuda(moe::launch_layer_few(T, k, H, I, E, x, topk_idx, topk_w, w13, w13_scales,
+                                           w2, w2_scales, fp8, out, out_dtype == MOE_OUT_F32,
+                                           workspace, err_word, stream));
+}
+
 moe_status moe_e4m3_encode_bits(uint32_t first, uint32_t count, uint8_t *codes,
                                 cudaStream_t stream)
 {

@@ -103,6 +103,35 @@ cudaError_t launch_dispatch_combine_flagged(int T, int H, int k, const void *x,
                                             uint64_t spin_limit_ns, int64_t skip_pair,
                                             uint32_t *err_word, cudaStream_t stream);
 
+// Router, expert products and the few-token layer.
+cudaError_t launch_route(int T, int E, int k, int groups, int keep, const void *logits,
+                         int64_t stride, bool f32, int32_t *topk_idx, float *topk_w,
+                         cudaStream_t stream);
+
+cudaError_t launch_route_backward(int T, int E, int k, const int32_t *topk_idx,
+                                  const float *topk_w, const float *dw, void *dlogits, bool f32,
+                                  uint32_t *err_word, cudaStream_t stream);
+
+cudaError_t launch_expert_gemm(int N, int K, int M, int E, const uint8_t *a_q, const float *a_s,
+                               const int32_t *offsets, const uint8_t *w_q, const float *w_s,
+                               bool transpose_w, void *out, bool out_f32, uint32_t *err_word,
+                               cudaStream_t stream);
+
+cudaError_t launch_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q, const float *a_s,
+                                 const int32_t *offsets, const uint8_t *w_q, const float *w_s,
+                                 uint8_t *h_q, float *h_s, uint32_t *err_word,
+                                 cudaStream_t stream);
+
+cudaError_t launch_expert_wgrad(int N, int M, int K, int E, const void *dy, const void *x,
+                                const int32_t *offsets, float *dw, uint32_t *err_word,
+                                cudaStream_t stream);
+
+size_t layer_few_workspace_bytes(int T, int k, int H, int I);
+cudaError_t launch_layer_few(int T, int k, int H, int I, int E, const void *x, const int32_t *idx,
+                             const float *topk_w, const void *w13, const float *s13,
+                             const void *w2, const float *s2, bool fp8, void *out, bool out_f32,
+                             void *workspace, uint32_t *err_word, cudaStream_t stream);
+
 // Launches `kernel` on `stream` with programmatic stream serialisation, so it
 // may become resident while the previous kernel in the stream is still running
 // (the kernel itself waits for that grid before touching global memory).

@@ -1,0 +1,298 @@
+// The top-k router and its gradient (sm_103a).
+//
+// HyperParallel-MoE, section 2.2: a router scores the experts and each token
+// goes to its k best.  Forward: s = logits (group-limited: all but the
+// experts of the best groups at -infinity), ids = the k largest, w_j =
+// exp(s_j - s_0) / sum_i exp(s_i - s_0).  Backward: ds_j = w_j (dw_j -
+// sum_i w_i dw_i).
+//
+// One warp owns a token: its logits sit in registers as order-preserving
+// 32-bit keys, so a round of the selection is a scan of the lane's keys and
+// two warp reductions in hardware (redux.sync: the largest key, then the
+// lowest id that has it).  Nothing is exchanged between warps.
+#include "common.cuh"
+#include "launch.h"
+
+#include <cuda_bf16.h>
+
+namespace moe {
+
+namespace {
+
+constexpr int ROUTE_THREADS = 128;
+constexpr uint32_t KEY_NEG_INF = 0x007fffffu;  // key of -infinity; 0 is below every key
+
+// Keys order as the values do; -0 and +0 share one, NaN has -infinity's.
+__device__ __forceinline__ uint32_t key_of(float f)
+{
+    if (!(f == f))
+        return KEY_NEG_INF;
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ float value_of(uint32_t key)
+{
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+template <typename L>
+struct Logits;
+template <>
+struct Logits<float> {
+    static __device__ float load(const float *p) { return ld_nc_f32(p); }
+    static __device__ void load4(const float *p, float f[4])
+    {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        f[0] = v.x;
+        f[1] = v.y;
+        f[2] = v.z;
+        f[3] = v.w;
+    }
+};
+template <>
+struct Logits<__nv_bfloat16> {
+    static __device__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    static __device__ void load4(const __nv_bfloat16 *p, float f[4])
+    {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        f[0] = bf16lo(v.x);
+        f[1] = bf16hi(v.x);
+        f[2] = bf16lo(v.y);
+        f[3] = bf16hi(v.y);
+    }
+};
+
+// Lane `lane`'s v-th expert: runs of P experts, lane after lane.
+template <int P>
+__device__ __forceinline__ int expert_of(int v, int lane)
+{
+    return (v / P) * 32 * P + lane * P + v % P;
+}
+
+template <int V, int P, typename L>
+__global__ void __launch_bounds__(ROUTE_THREADS)
+    route_kernel(const L *__restrict__ logits, int64_t stride, int T, int E, int k, int groups,
+                 int keep, int32_t *__restrict__ topk_idx, float *__restrict__ topk_w)
+{
+    wait_prior_grid();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (ROUTE_THREADS / 32) + (threadIdx.x >> 5);
+    if (t >= T)
+        return;
+    const L *row = logits + (int64_t)t * stride;
+    uint32_t key[V];
+    if constexpr (P == 4) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const int e = expert_of<P>(v, lane);
+            float f[4];
+            if (e < E)
+                Logits<L>::load4(row + e, f);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                key[v + i] = e < E ? key_of(f[i]) : 0u;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int e = expert_of<P>(v, lane);
+            key[v] = e < E ? key_of(Logits<L>::load(row + e)) : 0u;
+        }
+    }
+
+    if (groups > 1) {
+        const int size = E / groups;
+        uint32_t score = 0;  // lane g: group g's
+        for (int g = 0; g < groups; g++) {
+            const int lo = g * size, hi = lo + size;
+            uint32_t a = 0, b = 0;  // the lane's two largest keys of the group
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const int e = expert_of<P>(v, lane);
+                const uint32_t c = e >= lo && e < hi ? key[v] : 0u;
+                b = max(b, min(a, c));
+                a = max(a, c);
+            }
+            const uint32_t first = __reduce_max_sync(FULL_MASK, a);
+            const unsigned holds = __ballot_sync(FULL_MASK, a == first);
+            if (lane == __ffs(holds) - 1)
+                a = b;
+            const uint32_t second = __reduce_max_sync(FULL_MASK, a);
+            const float sum = size > 1 ? value_of(first) + value_of(second) : value_of(first);
+            if (lane == g)
+                score = key_of(sum);
+        }
+        unsigned kept = 0;
+        for (int i = 0; i < keep; i++) {
+            const uint32_t best = __reduce_max_sync(FULL_MASK, score);
+            const int g = __ffs(__ballot_sync(FULL_MASK, score == best)) - 1;
+            kept |= 1u << g;
+            if (lane == g)
+                score = 0;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int e = expert_of<P>(v, lane);
+            if (e < E && !((kept >> (e / size)) & 1))
+                key[v] = KEY_NEG_INF;
+        }
+    }
+
+    uint32_t top = 0, mine = 0;  // the largest key, and lane j's chosen one
+    int id = 0;
+    for (int j = 0; j < k; j++) {
+        uint32_t a = 0;
+        int at = 0;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (key[v] > a) {
+                a = key[v];
+                at = expert_of<P>(v, lane);
+            }
+        }
+        const uint32_t best = __reduce_max_sync(FULL_MASK, a);
+        const int win = (int)__reduce_min_sync(FULL_MASK, a == best ? (unsigned)at : 0xffffffffu);
+        if (j == 0)
+            top = best;
+        if (lane == j) {
+            mine = best;
+            id = win;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            if (expert_of<P>(v, lane) == win)
+                key[v] = 0;
+    }
+    float p = 0.0f;
+    if (lane < k && mine != KEY_NEG_INF)
+        p = mine == top ? 1.0f : expf(value_of(mine) - value_of(top));
+    float total = p;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        total += __shfl_xor_sync(FULL_MASK, total, d);
+    if (lane < k) {
+        topk_idx[(int64_t)t * k + lane] = id;
+        topk_w[(int64_t)t * k + lane] = total > 0.0f ? p / total : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// VEC: rows are whole 16-byte vectors.
+template <typename D, bool VEC>
+__global__ void __launch_bounds__(ROUTE_THREADS)
+    route_backward_kernel(const int32_t *__restrict__ topk_idx, const float *__restrict__ topk_w,
+                          const float *__restrict__ dw, int T, int E, int k,
+                          D *__restrict__ dlogits, uint32_t *err_word)
+{
+    wait_prior_grid();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (ROUTE_THREADS / 32) + (threadIdx.x >> 5);
+    if (t >= T)
+        return;
+    int id = -1;
+    float w = 0.0f, d = 0.0f;
+    if (lane < k) {
+        id = topk_idx[(int64_t)t * k + lane];
+        w = topk_w[(int64_t)t * k + lane];
+        d = dw[(int64_t)t * k + lane];
+        if (id < 0 || id >= E) {
+            report(err_word, MOE_ERRBIT_BAD_INDEX);
+            id = -1;
+        }
+    }
+    D *row = dlogits + (int64_t)t * E;
+    if constexpr (VEC) {
+        constexpr int W = 16 / sizeof(D);
+        for (int e = lane * W; e < E; e += 32 * W)
+            st_v4(row + e, make_uint4(0, 0, 0, 0));
+    } else {
+        for (int e = lane; e < E; e += 32)
+            put(row + e, 0.0f);
+    }
+    float s = w * d;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(FULL_MASK, s, o);
+    __syncwarp();  // the row's zeros come before its values
+    if (id >= 0)
+        put(row + id, w * (d - s));
+}
+
+template <int V, int P, typename L>
+cudaError_t route(int T, int E, int k, int groups, int keep, const void *logits, int64_t stride,
+                  int32_t *idx, float *w, cudaStream_t stream)
+{
+    constexpr int per = ROUTE_THREADS / 32;
+    return launch_pdl(route_kernel<V, P, L>, dim3((T + per - 1) / per), dim3(ROUTE_THREADS), 0,
+                      stream, static_cast<const L *>(logits), stride, T, E, k, groups, keep, idx,
+                      w);
+}
+
+template <typename L>
+cudaError_t route_for(int T, int E, int k, int groups, int keep, const void *logits,
+                      int64_t stride, int32_t *idx, float *w, cudaStream_t stream)
+{
+    // four experts a load where every row starts on such a boundary
+    const bool quads = E % 4 == 0 && stride % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(L)) == 0;
+    const int per_lane = (E + 31) / 32;
+#define MOE_ROUTE(V, P) route<V, P, L>(T, E, k, groups, keep, logits, stride, idx, w, stream)
+    if (quads) {
+        if (per_lane <= 4)
+            return MOE_ROUTE(4, 4);
+        if (per_lane <= 8)
+            return MOE_ROUTE(8, 4);
+        if (per_lane <= 16)
+            return MOE_ROUTE(16, 4);
+        return MOE_ROUTE(32, 4);
+    }
+    if (per_lane <= 2)
+        return MOE_ROUTE(2, 1);
+    if (per_lane <= 8)
+        return MOE_ROUTE(8, 1);
+    return MOE_ROUTE(32, 1);
+#undef MOE_ROUTE
+}
+
+template <typename D>
+cudaError_t route_backward(int T, int E, int k, const int32_t *idx, const float *w,
+                           const float *dw, void *dlogits, uint32_t *err_word,
+                           cudaStream_t stream)
+{
+    constexpr int per = ROUTE_THREADS / 32;
+    const bool vec = (E * sizeof(D)) % 16 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 16 == 0;
+    auto *kernel = vec ? route_backward_kernel<D, true> : route_backward_kernel<D, false>;
+    return launch_pdl(kernel, dim3((T + per - 1) / per), dim3(ROUTE_THREADS), 0, stream, idx, w,
+                      dw, T, E, k, static_cast<D *>(dlogits), err_word);
+}
+
+}  // namespace
+
+cudaError_t launch_route(int T, int E, int k, int groups, int keep, const void *logits,
+                         int64_t stride, bool f32, int32_t *topk_idx, float *topk_w,
+                         cudaStream_t stream)
+{
+    if (T == 0)
+        return cudaSuccess;
+    return f32 ? route_for<float>(T, E, k, groups, keep, logits, stride, topk_idx, topk_w, stream)
+               : route_for<__nv_bfloat16>(T, E, k, groups, keep, logits, stride, topk_idx, topk_w,
+                                          stream);
+}
+
+cudaError_t launch_route_backward(int T, int E, int k, const int32_t *topk_idx,
+                                  const float *topk_w, const float *dw, void *dlogits, bool f32,
+                                  uint32_t *err_word, cudaStream_t stream)
+{
+    if (T == 0)
+        return cudaSuccess;
+    return f32 ? route_backward<float>(T, E, k, topk_idx, topk_w, dw, dlogits, err_word, stream)
+               : route_backward<__nv_bfloat16>(T, E, k, topk_idx, topk_w, dw, dlogits, err_word,
+                                               stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,263 @@
+"""The router, the experts' products and the few-token layer: what stands before
+the layout and between dispatch and combine.
+
+Bindings of moe_route, moe_route_backward, moe_expert_gemm, moe_expert_swiglu,
+moe_expert_wgrad and moe_layer_few, in the manner of the package's other calls
+(and re-exported by it), and `MoELayer`, which runs them together with layout,
+dispatch and combine.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import (MOE_FEW_MAX_PAIRS, MOE_FEW_MAX_TOKENS, MOE_OUT_BF16, MOE_OUT_F32, MOE_W_BF16,
+               MOE_W_E4M3, _check, _lib, _ptr, _stream, _want, moe_combine,
+               moe_layout_dispatch_quant, moe_layout_workspace_bytes, new_error_word,
+               new_workspace)
+
+_CODES = {torch.bfloat16: MOE_OUT_BF16, torch.float32: MOE_OUT_F32}
+
+
+def _code(dtype: torch.dtype, name: str) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    return code
+
+
+class Routing(NamedTuple):
+    topk_idx: torch.Tensor  # int32 [T, k]
+    topk_w: torch.Tensor    # fp32 [T, k]
+
+
+def moe_route(logits: torch.Tensor, k: int, *, groups: int = 1, topk_groups: int = 1,
+              out: Optional[Routing] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> Routing:
+    """Ids of the k largest logits of each row and their softmax weights
+    (group-limited with groups > 1).  logits is bf16 or fp32 [T, E]; its rows
+    may be strided."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    T, E = logits.shape
+    code = _code(logits.dtype, "logits")
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    stride = logits.stride(0) if T > 1 else E
+    if out is None:
+        out = Routing(torch.empty((T, k), dtype=torch.int32, device=logits.device),
+                      torch.empty((T, k), dtype=torch.float32, device=logits.device))
+    else:
+        _want(out.topk_idx, "topk_idx", torch.int32, (T, k))
+        _want(out.topk_w, "topk_w", torch.float32, (T, k))
+    _check(_lib.moe_route(T, E, k, groups, topk_groups, _ptr(logits), stride, code,
+                          _ptr(out.topk_idx), _ptr(out.topk_w), _stream(stream)), "moe_route")
+    return out
+
+
+def moe_route_backward(topk_idx: torch.Tensor, topk_w: torch.Tensor, dw: torch.Tensor, E: int, *,
+                       out_dtype: torch.dtype = torch.float32,
+                       dlogits: Optional[torch.Tensor] = None,
+                       err_word: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of moe_route's weights to its logits: dlogits [T, E]."""
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    T, k = topk_idx.shape
+    _want(topk_idx, "topk_idx", torch.int32)
+    _want(topk_w, "topk_w", torch.float32, (T, k))
+    _want(dw, "dw", torch.float32, (T, k))
+    code = _code(out_dtype, "out_dtype")
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=out_dtype, device=topk_idx.device)
+    else:
+        _want(dlogits, "dlogits", out_dtype, (T, E))
+    _check(_lib.moe_route_backward(T, E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(dw),
+                                   _ptr(dlogits), code, _ptr(err_word), _stream(stream)),
+           "moe_route_backward")
+    return dlogits
+
+
+def _rows_and_weights(a_q, a_scales, expert_offsets, w_q, w_scales, transpose_w):
+    """Checks a product's arguments; returns (N, K, outputs, E)."""
+    if a_q.dim() != 2 or w_q.dim() != 3:
+        raise ValueError("a_q must be [N, K] and w_q 3-dimensional")
+    N, K = a_q.shape
+    E, rows, cols = w_q.shape
+    outs = cols if transpose_w else rows
+    _want(a_q, "a_q", torch.uint8)
+    _want(a_scales, "a_scales", torch.float32, (N, K // 128))
+    _want(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _want(w_q, "w_q", torch.uint8, (E, K, outs) if transpose_w else (E, outs, K))
+    _want(w_scales, "w_scales", torch.float32, (E, (rows + 127) // 128, (cols + 127) // 128))
+    return N, K, outs, E
+
+
+def moe_expert_gemm(a_q: torch.Tensor, a_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                    w_q: torch.Tensor, w_scales: torch.Tensor, *, transpose_w: bool = False,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    err_word: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Every expert's FP8 product over its segment of rows: [N, M].
+
+    a_q, a_scales: E4M3 codes [N, K] and 1x128 scales (moe_dispatch_quant).
+    w_q, w_scales: codes [E, M, K] and 128x128 scales, or with transpose_w
+    [E, K, M], the gradient to the rows of a forward product."""
+    N, K, M, E = _rows_and_weights(a_q, a_scales, expert_offsets, w_q, w_scales, transpose_w)
+    code = _code(out_dtype, "out_dtype")
+    if out is None:
+        out = torch.empty((N, M), dtype=out_dtype, device=a_q.device)
+    else:
+        _want(out, "out", out_dtype, (N, M))
+    _check(_lib.moe_expert_gemm(N, K, M, E, _ptr(a_q), _ptr(a_scales), _ptr(expert_offsets),
+                                _ptr(w_q), _ptr(w_scales), int(transpose_w), _ptr(out), code,
+                                _ptr(err_word), _stream(stream)), "moe_expert_gemm")
+    return out
+
+
+def moe_expert_swiglu(a_q: torch.Tensor, a_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                      w_q: torch.Tensor, w_scales: torch.Tensor, *,
+                      h_q: Optional[torch.Tensor] = None,
+                      h_scales: Optional[torch.Tensor] = None,
+                      err_word: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """Gate and up products (w_q [E, 2I, K]), SwiGLU, and the quantisation of the
+    result.  Returns (h_q uint8 [N, I], h_scales fp32 [N, I/128])."""
+    N, K, wide, E = _rows_and_weights(a_q, a_scales, expert_offsets, w_q, w_scales, False)
+    if wide % 2:
+        raise ValueError("w_q must hold as many gate rows as up rows")
+    inner = wide // 2
+    if h_q is None:
+        h_q = torch.empty((N, inner), dtype=torch.uint8, device=a_q.device)
+    else:
+        _want(h_q, "h_q", torch.uint8, (N, inner))
+    if h_scales is None:
+        h_scales = torch.empty((N, inner // 128), dtype=torch.float32, device=a_q.device)
+    else:
+        _want(h_scales, "h_scales", torch.float32, (N, inner // 128))
+    _check(_lib.moe_expert_swiglu(N, K, inner, E, _ptr(a_q), _ptr(a_scales),
+                                  _ptr(expert_offsets), _ptr(w_q), _ptr(w_scales), _ptr(h_q),
+                                  _ptr(h_scales), _ptr(err_word), _stream(stream)),
+           "moe_expert_swiglu")
+    return h_q, h_scales
+
+
+def moe_expert_wgrad(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor, *,
+                     dw: Optional[torch.Tensor] = None,
+                     err_word: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Every expert's weight gradient dy^T x over its rows: fp32 [E, M, K]."""
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError("dy must be [N, M] and x [N, K]")
+    N, M = dy.shape
+    K = x.shape[1]
+    E = expert_offsets.numel() - 1
+    _want(dy, "dy", torch.bfloat16)
+    _want(x, "x", torch.bfloat16, (N, K))
+    _want(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    if dw is None:
+        dw = torch.empty((E, M, K), dtype=torch.float32, device=dy.device)
+    else:
+        _want(dw, "dw", torch.float32, (E, M, K))
+    _check(_lib.moe_expert_wgrad(N, M, K, E, _ptr(dy), _ptr(x), _ptr(expert_offsets), _ptr(dw),
+                                 _ptr(err_word), _stream(stream)), "moe_expert_wgrad")
+    return dw
+
+
+def moe_layer_few_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
+    return int(_lib.moe_layer_few_workspace_bytes(T, k, H, I))
+
+
+def moe_layer_few(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                  w13: torch.Tensor, w2: torch.Tensor, *,
+                  w13_scales: Optional[torch.Tensor] = None,
+                  w2_scales: Optional[torch.Tensor] = None,
+                  out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  err_word: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """A whole expert layer for at most MOE_FEW_MAX_TOKENS tokens: [T, H].
+
+    w13 [E, 2I, H] and w2 [E, H, I] are bf16, or uint8 E4M3 codes with fp32
+    scales of 128x128 blocks."""
+    if x.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x must be [T, H], topk_idx [T, k], w13 [E, 2I, H] and w2 [E, H, I]")
+    T, H = x.shape
+    k = topk_idx.shape[1]
+    E, _, inner = w2.shape
+    _want(x, "x", torch.bfloat16)
+    _want(topk_idx, "topk_idx", torch.int32, (T, k))
+    _want(topk_w, "topk_w", torch.float32, (T, k))
+    fp8 = w13.dtype == torch.uint8
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    _want(w13, "w13", kind, (E, 2 * inner, H))
+    _want(w2, "w2", kind, (E, H, inner))
+    if fp8:
+        if w13_scales is None or w2_scales is None:
+            raise ValueError("E4M3 weights need w13_scales and w2_scales")
+        _want(w13_scales, "w13_scales", torch.float32, (E, 2 * inner // 128, H // 128))
+        _want(w2_scales, "w2_scales", torch.float32, (E, H // 128, inner // 128))
+    elif w13_scales is not None or w2_scales is not None:
+        raise ValueError("bf16 weights take no scales")
+    code = _code(out_dtype, "out_dtype")
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    else:
+        _want(out, "out", out_dtype, (T, H))
+    if workspace is None:
+        workspace = torch.empty(moe_layer_few_workspace_bytes(T, k, H, inner), dtype=torch.uint8,
+                                device=x.device)
+    _check(_lib.moe_layer_few(T, k, H, inner, E, _ptr(x), _ptr(topk_idx), _ptr(topk_w),
+                              _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
+                              MOE_W_E4M3 if fp8 else MOE_W_BF16, _ptr(out), code,
+                              _ptr(workspace), workspace.numel() * workspace.element_size(),
+                              _ptr(err_word), _stream(stream)), "moe_layer_few")
+    return out
+
+
+class MoELayer:
+    """A mixture-of-experts layer: router, layout, FP8 dispatch, the experts'
+    products and combine for long batches, moe_layer_few for short ones.
+
+    Holds the experts' E4M3 weights and scales (w13 [E, 2I, H], w2 [E, H, I],
+    gate rows of w13 first).  Calling it with x [T, H] bf16 and the router's
+    logits [T, E] returns [T, H]; device-side errors collect in `err_word`.
+    """
+
+    def __init__(self, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
+                 w2_scales: torch.Tensor, k: int, *, groups: int = 1, topk_groups: int = 1):
+        if w13.dtype != torch.uint8 or w2.dtype != torch.uint8:
+            raise TypeError("w13 and w2 must be uint8 E4M3 codes")
+        self.w13, self.w13_scales, self.w2, self.w2_scales = w13, w13_scales, w2, w2_scales
+        self.k, self.groups, self.topk_groups = k, groups, topk_groups
+        self.err_word = new_error_word(w13.device)
+        self._layout_ws: Optional[torch.Tensor] = None
+
+    def few(self, T: int) -> bool:
+        """Whether a batch of T tokens takes the two-kernel form."""
+        return T <= MOE_FEW_MAX_TOKENS and T * self.k <= MOE_FEW_MAX_PAIRS
+
+    def __call__(self, x: torch.Tensor, logits: torch.Tensor, *,
+                 out_dtype: torch.dtype = torch.bfloat16,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        T, E = logits.shape
+        err = self.err_word
+        idx, w = moe_route(logits, self.k, groups=self.groups, topk_groups=self.topk_groups,
+                           stream=stream)
+        if self.few(T):
+            return moe_layer_few(x, idx, w, self.w13, self.w2, w13_scales=self.w13_scales,
+                                 w2_scales=self.w2_scales, out_dtype=out_dtype, err_word=err,
+                                 stream=stream)
+        need = moe_layout_workspace_bytes(T, self.k, E)
+        if self._layout_ws is None or self._layout_ws.numel() < need:
+            self._layout_ws = new_workspace(need, x.device)
+        lay, q, s = moe_layout_dispatch_quant(x, idx, E, 1, workspace=self._layout_ws,
+                                              err_word=err, stream=stream)
+        h, hs = moe_expert_swiglu(q, s, lay.expert_offsets, self.w13, self.w13_scales,
+                                  err_word=err, stream=stream)
+        y = moe_expert_gemm(h, hs, lay.expert_offsets, self.w2, self.w2_scales, err_word=err,
+                            stream=stream)
+        return moe_combine(y, lay.slot_of, w, out_dtype=out_dtype, err_word=err, stream=stream)

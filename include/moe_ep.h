@@ -532,6 +532,159 @@ MOE_API moe_status moe_layout_noalloc(int T, int k, int E, int R, const int32_t 
                               int32_t *rank_offsets, int32_t *slot_of, int32_t *src_of,
                               uint32_t *err_word, cudaStream_t stream);
 
+/* element type of expert weights */
+typedef enum moe_weight_dtype { MOE_W_BF16 = 0, MOE_W_E4M3 = 1 } moe_weight_dtype;
+
+/* limits of the few-token layer, and the largest k of the router */
+#define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_MAX_PAIRS 512
+#define MOE_MAX_TOPK 32
+
+/*
+ * moe_route -- the top-k router: ids and softmax weights from the logits.
+ *
+ * HyperParallel-MoE, section 2.2 (a router scores the experts, each token goes
+ * to its k best and their outputs are weighted by the routing scores);
+ * the group-limited choice is that of RailWave's GLM-4.5-Air replay.
+ *
+ *   logits    [T, E]  bf16 (logits_dtype MOE_OUT_BF16) or fp32 (MOE_OUT_F32);
+ *                     row t starts at element t * logits_stride
+ *   topk_idx  [T, k]  out: int32 ids of the k largest logits, largest first,
+ *                     ties to the lower id (-0 and +0 tie)
+ *   topk_w    [T, k]  out: fp32 softmax over the k chosen logits
+ *
+ * groups > 1 cuts the experts into that many equal runs, scores each by the sum
+ * (one fp32 addition) of its two largest logits, keeps the topk_groups best
+ * (ties to the lower group) and takes every other expert's logit as -infinity.
+ * A group with fewer than two experts left unmasked (of two or more) therefore
+ * scores -infinity.
+ * A logit of -infinity masks its expert: weight 0, chosen only when nothing
+ * else is left (lowest ids first).  A row with nothing left has weights 0.
+ * NaN counts as -infinity.  Infinite positive logits share the weight equally.
+ *
+ * 1 <= E <= MOE_MAX_EXPERTS, E % groups == 0, 1 <= topk_groups <= groups <= 32
+ * (more groups, or a larger E or k: MOE_ERR_UNSUPPORTED), 1 <= k <= min(MOE_MAX_TOPK, topk_groups * E / groups), logits_stride >= E.
+ */
+MOE_API moe_status moe_route(int T, int E, int k, int groups, int topk_groups, const void *logits,
+                     int64_t logits_stride, int logits_dtype, int32_t *topk_idx, float *topk_w,
+                     cudaStream_t stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route's weights to its logits.
+ *
+ *   topk_idx, topk_w  [T, k]  from moe_route
+ *   dw                [T, k]  fp32 gradient of topk_w (moe_combine_backward's dw)
+ *   dlogits           [T, E]  out: fp32 or bf16 (dlogits_dtype)
+ *
+ * dlogits[t, idx[t,j]] = w[t,j] * (dw[t,j] - sum_i w[t,i] * dw[t,i]); 0 for every
+ * expert that was not chosen.  The ids of one token differ (moe_route's do).  An
+ * id outside [0, E) sets MOE_ERRBIT_BAD_INDEX and is skipped.
+ */
+MOE_API moe_status moe_route_backward(int T, int E, int k, const int32_t *topk_idx,
+                              const float *topk_w, const float *dw, void *dlogits,
+                              int dlogits_dtype, uint32_t *err_word, cudaStream_t stream);
+
+/*
+ * moe_expert_gemm -- every expert's product over its segment of rows, FP8 with
+ * block scales.
+ *
+ * HyperParallel-MoE, section 2.2 (the experts' matrix products between Dispatch
+ * and Combine); UBEP, Table 3 (W8A8).  With e the segment of row n:
+ *
+ *   out[n, o] = sum_b a_scales[n, b] * S(e, o, b) * sum_{i in block b} a[n, i] * W(e, o, i)
+ *
+ * where block b holds the inputs 128 b .. 128 b + 127.
+ *
+ *   a_q       [N, K]      E4M3 codes of the rows (moe_dispatch_quant's recv_q)
+ *   a_scales  [N, K/128]  fp32 (its recv_scales)
+ *   expert_offsets [E+1]  int32, from moe_layout: expert e owns the rows
+ *                         expert_offsets[e] .. expert_offsets[e+1] - 1.  Rows that
+ *                         no segment holds are not written
+ *   w_q, w_scales         transpose_w == 0: W(e, o, i) = w_q[e, o, i], [E, M, K], and
+ *                         S(e, o, b) = w_scales[e, o/128, b], [E, ceil(M/128), K/128];
+ *                         transpose_w == 1: W(e, o, i) = w_q[e, i, o], [E, K, M], and
+ *                         S(e, o, b) = w_scales[e, b, o/128], [E, K/128, ceil(M/128)]
+ *   out       [N, M]      out: bf16 or fp32 (out_dtype)
+ *
+ * transpose_w == 1 is the gradient to the rows: with a = the quantised gradient of
+ * a forward product's output and the same w_q [E, K, M] that the forward call took
+ * as its [E, M', K'], out is the gradient of its input.  Products are exact, sums
+ * fp32, one rounding to out's type.  K % 128 == 0, M % 16 == 0, N >= 0.  A pair
+ * of offsets that descends or leaves [0, N] sets MOE_ERRBIT_BAD_INDEX and its
+ * segment is skipped.  Payload and scale arrays 16-byte aligned.
+ */
+MOE_API moe_status moe_expert_gemm(int N, int K, int M, int E, const uint8_t *a_q,
+                           const float *a_scales, const int32_t *expert_offsets,
+                           const uint8_t *w_q, const float *w_scales, int transpose_w, void *out,
+                           int out_dtype, uint32_t *err_word, cudaStream_t stream);
+
+/*
+ * moe_expert_swiglu -- the gate and up products of every expert, SwiGLU, and
+ * the block quantisation of the result, in one kernel.
+ *
+ * With y the [N, 2I] product of moe_expert_gemm (transpose_w == 0, M = 2I) before
+ * its rounding, g = y[n, c], u = y[n, I + c]: h[n, c] = g / (1 + exp(-g)) * u in
+ * fp32, quantised in blocks of 1 x 128 as moe_dispatch_quant does.
+ *
+ *   w_q       [E, 2I, K]         gate rows 0 .. I-1, up rows I .. 2I-1
+ *   w_scales  [E, 2I/128, K/128]
+ *   h_q       [N, I]             out: E4M3 codes
+ *   h_scales  [N, I/128]         out: fp32
+ *
+ * K % 128 == 0, I % 128 == 0; otherwise as moe_expert_gemm.
+ */
+MOE_API moe_status moe_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q,
+                             const float *a_scales, const int32_t *expert_offsets,
+                             const uint8_t *w_q, const float *w_scales, uint8_t *h_q,
+                             float *h_scales, uint32_t *err_word, cudaStream_t stream);
+
+/*
+ * moe_expert_wgrad -- the gradient of every expert's weights.
+ *
+ *   dy  [N, M]     bf16 gradient of the product's output, rows by segment
+ *   x   [N, K]     bf16 input rows (moe_dispatch's recv)
+ *   dw  [E, M, K]  out: fp32, dw[e, o, i] = sum of dy[n, o] * x[n, i] over e's
+ *                  rows in fp32; zeros for an expert without rows
+ *
+ * M % 8 == 0, K % 8 == 0.  Offsets as in moe_expert_gemm (a skipped segment's dw is
+ * zeros).
+ */
+MOE_API moe_status moe_expert_wgrad(int N, int M, int K, int E, const void *dy, const void *x,
+                            const int32_t *expert_offsets, float *dw, uint32_t *err_word,
+                            cudaStream_t stream);
+
+/*
+ * moe_layer_few -- a whole mixture-of-experts layer for a few tokens, in two
+ * kernels: no layout, no dispatched copies, every chosen expert's weights read
+ * once.
+ *
+ *   out[t] = sum_j topk_w[t,j] * W2_e ( silu(Wg_e x[t]) * (Wu_e x[t]) ),  e = topk_idx[t,j]
+ *
+ *   x         [T, H]      bf16
+ *   topk_idx, topk_w [T, k]
+ *   w13       [E, 2I, H]  gate rows 0 .. I-1, up rows I .. 2I-1
+ *   w2        [E, H, I]
+ *             bf16 (weight_dtype MOE_W_BF16; w13_scales, w2_scales unused), or
+ *             E4M3 codes (MOE_W_E4M3) with fp32 scales of 128 x 128 blocks,
+ *             w13_scales [E, 2I/128, H/128], w2_scales [E, H/128, I/128]
+ *   out       [T, H]      out: bf16 or fp32
+ *   workspace moe_layer_few_workspace_bytes(T, k, H, I) bytes, 16-byte aligned;
+ *             needs no initialisation, holds nothing between calls
+ *
+ * Activations stay bf16 (x) and, between the products, two bf16 terms of the
+ * fp32 value; sums are fp32 in an order that depends on the arguments' sizes and the
+ * routing alone.  T <= MOE_FEW_MAX_TOKENS, T*k <= MOE_FEW_MAX_PAIRS, k <= MOE_MAX_TOPK
+ * (more: MOE_ERR_UNSUPPORTED); H and I multiples of 8, of 128 for E4M3.  A token
+ * may name an expert twice.  Ids outside [0, E) set MOE_ERRBIT_BAD_INDEX and add
+ * nothing.
+ */
+MOE_API size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I);
+MOE_API moe_status moe_layer_few(int T, int k, int H, int I, int E, const void *x,
+                         const int32_t *topk_idx, const float *topk_w, const void *w13,
+                         const float *w13_scales, const void *w2, const float *w2_scales,
+                         int weight_dtype, void *out, int out_dtype, void *workspace,
+                         size_t workspace_bytes, uint32_t *err_word, cudaStream_t stream);
+
 /*
  * moe_read_error -- synchronise `stream`, read the device error word into
  * *bits_out (may be NULL), clear it when `clear` is non-zero, and return the
