@@ -4,133 +4,362 @@
 // out[n, o] = sum_b sa[n, b] * S(e, o, b) * sum_{i in b} a[n, i] * W(e, o, i),
 // with e the segment that holds row n and b the 128-wide blocks of the inputs.
 //
-// One CTA owns 32 rows of one expert and 128 outputs (for SwiGLU 128 gate
-// and the matching 128 up outputs, so that a row's quantisation block is the
-// CTA's own).  Codes widen to fp32 in shared memory, each block's products are
-// summed and then scaled into the running fp32 sums.
-#include <cuda_fp8.h>
+// The scale of a product changes with every 128 inputs and differs from row to
+// row by any fp32 factor, so the tensor core cannot sum over blocks: it
+// multiplies one block (four tcgen05.mma of K = 32 into tensor memory), and the
+// promotion warps read the 128 x 256 fp32 sums back, scale them and add them to
+// the running sums in their registers (one packed fused multiply-add for two
+// outputs) while the tensor core fills the other half of tensor memory.
+//
+// One persistent CTA per SM, 128 rows x 256 outputs a tile:
+//   warps 0-7   promotion: warp w holds rows 32 (w % 4) .. +31, a thread one
+//               row and 2 x 64 outputs; then the epilogue
+//   warp 8      (with 9 to 11 a warpgroup of few registers) tensor copies: a block of the rows (boxes of 32 rows, only
+//               those of the segment) and of the weights (2 x 128 outputs)
+//   warp 9      issues the MMAs
+// For SwiGLU the two 128-output halves are gate and up of the same 128
+// channels, which makes a row's quantisation block the tile's own.
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "launch.h"
 #include "segments.cuh"
+#include "tcgen05.cuh"
+#include "tensormap.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int GEMM_THREADS = 256;
-constexpr int GEMM_ROWS = 32;
-constexpr int GEMM_COLS = 128;
-constexpr int GEMM_STEP = 32;
+enum { OUT_BF16, OUT_F32, OUT_SWIGLU };
 
-__device__ __forceinline__ float e4m3(uint8_t c)
+constexpr int G_THREADS = 384;  // three warpgroups
+constexpr int G_PROMOTE = 256;  // threads of the promotion warps
+constexpr int G_ROWS = 128;
+constexpr int G_COLS = 256;
+constexpr int G_BOX = 32;  // rows of one tensor copy of a
+constexpr int G_STAGES = 4;
+constexpr int G_A_BYTES = G_ROWS * 128;
+constexpr int G_B_HALF = 128 * 128;
+constexpr int G_STAGE = G_A_BYTES + 2 * G_B_HALF;
+
+struct GemmShared {
+    uint64_t full[G_STAGES], empty[G_STAGES];
+    uint64_t sums_full[2], sums_empty[2];
+    uint32_t tmem;
+    float amax[2][G_ROWS];
+    Segments seg;
+};
+
+constexpr size_t G_SMEM = 1024 + (size_t)G_STAGES * G_STAGE + sizeof(GemmShared);
+
+struct GemmArgs {
+    int N, kb, M, E, col_tiles;  // kb: blocks of 128 inputs; M: outputs (SwiGLU: I)
+    const float *a_s, *w_s;
+    const int32_t *offsets;
+    void *out;
+    float *out_s;
+    uint32_t *err_word;
+};
+
+struct GemmTile {
+    int expert, row, rows, col;
+};
+
+__device__ __forceinline__ GemmTile gemm_tile(const Segments &s, const GemmArgs &g, int tile)
 {
-    __nv_fp8_e4m3 v;
-    v.__x = c;
-    return static_cast<float>(v);
+    GemmTile t;
+    t.expert = expert_of_tile(s, g.E, tile / g.col_tiles);
+    const int before = s.first[t.expert], tiles = s.first[t.expert + 1] - before;
+    const int local = tile - before * g.col_tiles;
+    // the expert's row tiles vary fastest: neighbours in time share its weights
+    t.row = s.lo[t.expert] + local % tiles * G_ROWS;
+    t.rows = min(G_ROWS, s.hi[t.expert] - t.row);
+    t.col = local / tiles;
+    return t;
 }
 
-enum { OUT_ROWS_BF16, OUT_ROWS_F32, OUT_SWIGLU };
+template <int OUT, bool TRANS>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_w, const GemmArgs g)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    GemmShared &sh = *reinterpret_cast<GemmShared *>(stages + G_STAGES * G_STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G_STAGES; i++) {
+            mbar_init(smem_addr(&sh.full[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_addr(&sh.sums_full[i]), 1);
+            mbar_init(smem_addr(&sh.sums_empty[i]), G_PROMOTE / 32);
+        }
+        mbar_fence_init();
+        prefetch_map(&map_a);
+        prefetch_map(&map_w);
+    }
+    if (warp == 9)
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+    wait_prior_grid();
+    load_segments(sh.seg, g.offsets, g.E, g.N, G_ROWS, blockIdx.x == 0 ? g.err_word : nullptr);
+    allow_next_grid();
+    tcgen05_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const int tiles = sh.seg.first[g.E] * g.col_tiles;
+    bool ok = true;  // false once one of this thread's waits gave up
+
+    // the promotion warps hold 128 running sums each thread: the third
+    // warpgroup gives them its registers (168 at launch: 72 + 2 x 216 = 3 x 168)
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                const GemmTile t = gemm_tile(sh.seg, g, tile);
+                const int boxes = (t.rows + G_BOX - 1) / G_BOX;
+                const int c0 = OUT == OUT_SWIGLU ? t.col * 128 : t.col * G_COLS;
+                const int c1 = OUT == OUT_SWIGLU ? g.M + c0 : c0 + 128;
+                for (int b = 0; b < g.kb; b++) {
+                    if (!(ok = mbar_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
+                        break;
+                    const uint32_t bar = smem_addr(&sh.full[s]);
+                    const uint32_t at = smem_addr(stages + s * G_STAGE);
+                    mbar_arrive_expect_tx(bar, boxes * G_BOX * 128 + 2 * G_B_HALF);
+                    for (int i = 0; i < boxes; i++)
+                        tensor_g2s(at + i * G_BOX * 128, &map_a, b * 128, t.row + i * G_BOX, 0,
+                                   bar);
+                    if (TRANS) {
+                        tensor_g2s(at + G_A_BYTES, &map_w, c0, b * 128, t.expert, bar);
+                        tensor_g2s(at + G_A_BYTES + G_B_HALF, &map_w, c1, b * 128, t.expert, bar);
+                    } else {
+                        tensor_g2s(at + G_A_BYTES, &map_w, b * 128, c0, t.expert, bar);
+                        tensor_g2s(at + G_A_BYTES + G_B_HALF, &map_w, b * 128, c1, t.expert, bar);
+                    }
+                    issued++;
+                    if (++s == G_STAGES) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // copies still in flight land before the CTA may end
+            for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
+                ok = mbar_wait(smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+        }
+    }
+    if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = mma_desc(G_ROWS, G_COLS, 0, false, TRANS);
+            int s = 0, d = 0;
+            uint32_t phase = 0, d_phase = 0;
+            int64_t issued = 0;
+            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                for (int b = 0; b < g.kb; b++) {
+                    if (!(ok = mbar_wait(smem_addr(&sh.sums_empty[d]), d_phase ^ 1) &&
+                               mbar_wait(smem_addr(&sh.full[s]), phase)))
+                        break;
+                    tcgen05_after_sync();
+                    const uint32_t at = smem_addr(stages + s * G_STAGE);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        // rows of 128 inputs: the next 32 are 32 bytes on.  Outputs
+                        // contiguous: 32 rows of 128 bytes on
+                        const uint64_t da = smem_desc(at + i * 32, 16, 1024);
+                        const uint64_t db =
+                            TRANS ? smem_desc(at + G_A_BYTES + i * 4096, G_B_HALF, 1024)
+                                  : smem_desc(at + G_A_BYTES + i * 32, 16, 1024);
+                        mma_f8(tmem + d * G_COLS, da, db, idesc, i > 0);
+                    }
+                    tcgen05_commit(smem_addr(&sh.empty[s]));
+                    tcgen05_commit(smem_addr(&sh.sums_full[d]));
+                    issued++;
+                    if (++s == G_STAGES) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    if (++d == 2) {
+                        d = 0;
+                        d_phase ^= 1;
+                    }
+                }
+            }
+            // and so do the MMAs' arrivals
+            for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
+                ok = mbar_wait(smem_addr(&sh.empty[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int half = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+        const int ob = (g.M + 127) / 128;  // 128-output blocks of the weights' scales
+        int d = 0;
+        uint32_t d_phase = 0;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            const GemmTile t = gemm_tile(sh.seg, g, tile);
+            const bool busy = quarter * 32 < t.rows;  // of the warp
+            const float *sa = g.a_s + (int64_t)(t.row + min(r, t.rows - 1)) * g.kb;
+            const int o0 = OUT == OUT_SWIGLU ? t.col : 2 * t.col;
+            const int o1 = OUT == OUT_SWIGLU ? g.M / 128 + t.col : min(o0 + 1, ob - 1);
+            const int blocks = OUT == OUT_SWIGLU ? 2 * ob : ob;
+            const float *sw = g.w_s + (int64_t)t.expert * blocks * g.kb;
+            const int64_t w0 = TRANS ? o0 : (int64_t)o0 * g.kb, w1 = TRANS ? o1 : (int64_t)o1 * g.kb;
+            const int64_t wstep = TRANS ? blocks : 1;
+            float2 acc[2][32];
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                acc[0][i] = acc[1][i] = make_float2(0.0f, 0.0f);
+            float s0 = 0.0f, s1 = 0.0f, sr = sa[0];
+            for (int b = 0; b < g.kb; b++) {
+                if ((b & 31) == 0) {  // the weights' scales of the next 32 blocks, one a lane
+                    const int at = min(b + lane, g.kb - 1);
+                    s0 = sw[w0 + at * wstep];
+                    s1 = sw[w1 + at * wstep];
+                }
+                const float f0 = sr * __shfl_sync(FULL_MASK, s0, b & 31);
+                const float f1 = sr * __shfl_sync(FULL_MASK, s1, b & 31);
+                sr = sa[min(b + 1, g.kb - 1)];
+                ok = __all_sync(FULL_MASK, mbar_wait(smem_addr(&sh.sums_full[d]), d_phase));
+                if (!ok)
+                    break;
+                if (busy) {
+                    tcgen05_after_sync();
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        uint32_t p[32];
+                        tmem_ld32(mine + d * G_COLS + (q >> 1) * 128 + (q & 1) * 32, p);
+                        tmem_wait_ld();
+                        const float f = q >> 1 ? f1 : f0;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            float2 &c = acc[q >> 1][(q & 1) * 16 + i];
+                            c = fma2(make_float2(__uint_as_float(p[2 * i]),
+                                                 __uint_as_float(p[2 * i + 1])),
+                                     make_float2(f, f), c);
+                        }
+                    }
+                    tcgen05_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.sums_empty[d]));
+                if (++d == 2) {
+                    d = 0;
+                    d_phase ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            const int64_t n = t.row + r;
+            if constexpr (OUT == OUT_SWIGLU) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 32; i++) {
+                    const float2 v = acc[0][i];
+                    acc[0][i].x = v.x / (1.0f + expf(-v.x)) * acc[1][i].x;
+                    acc[0][i].y = v.y / (1.0f + expf(-v.y)) * acc[1][i].y;
+                    amax = fmaxf(amax, fmaxf(fabsf(acc[0][i].x), fabsf(acc[0][i].y)));
+                }
+                // the block's other 64 channels are with the warp four on
+                sh.amax[half][r] = amax;
+                named_barrier(1 + quarter, 64);
+                amax = fmaxf(amax, sh.amax[half ^ 1][r]);
+                named_barrier(1 + quarter, 64);
+                if (r < t.rows) {
+                    float scale, inv;
+                    block_scale(amax, scale, inv);
+                    uint8_t *to = static_cast<uint8_t *>(g.out) + n * g.M + t.col * 128 + half * 64;
+#pragma unroll
+                    for (int v = 0; v < 4; v++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float2 a = acc[0][v * 8 + 2 * i], b = acc[0][v * 8 + 2 * i + 1];
+                            w[i] = __nv_cvt_float2_to_fp8x2(
+                                       make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)),
+                                       __NV_SATFINITE, __NV_E4M3) |
+                                   (uint32_t)__nv_cvt_float2_to_fp8x2(
+                                       make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)),
+                                       __NV_SATFINITE, __NV_E4M3)
+                                       << 16;
+                        }
+                        st_v4(to + v * 16, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                    if (half == 0)
+                        g.out_s[n * ob + t.col] = scale;
+                }
+            } else if (r < t.rows) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int o = t.col * G_COLS + h * 128 + half * 64;
+                    if constexpr (OUT == OUT_F32) {
+                        float *to = static_cast<float *>(g.out) + n * g.M + o;
+#pragma unroll
+                        for (int v = 0; v < 16; v++)
+                            if (o + v * 4 < g.M)
+                                st_v4(to + v * 4,
+                                      make_uint4(__float_as_uint(acc[h][2 * v].x),
+                                                 __float_as_uint(acc[h][2 * v].y),
+                                                 __float_as_uint(acc[h][2 * v + 1].x),
+                                                 __float_as_uint(acc[h][2 * v + 1].y)));
+                    } else {
+                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(g.out) + n * g.M + o;
+#pragma unroll
+                        for (int v = 0; v < 8; v++) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const __nv_bfloat162 b = __float22bfloat162_rn(acc[h][v * 4 + i]);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            if (o + v * 8 < g.M)
+                                st_v4(to + v * 8, make_uint4(w[0], w[1], w[2], w[3]));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!ok)
+        report(g.err_word, MOE_ERRBIT_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    if (warp == 9)
+        tmem_free(tmem, 512);
+}
 
 template <int OUT, bool TRANS>
-__global__ void __launch_bounds__(GEMM_THREADS)
-    expert_gemm_kernel(int N, int K, int M, int E, const uint8_t *__restrict__ a_q,
-                       const float *__restrict__ a_s, const int32_t *__restrict__ offsets,
-                       const uint8_t *__restrict__ w_q, const float *__restrict__ w_s,
-                       void *__restrict__ out, float *__restrict__ out_s, uint32_t *err_word)
+cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uint8_t *w_q,
+                     cudaStream_t stream)
 {
-    constexpr int HALVES = OUT == OUT_SWIGLU ? 2 : 1;
-    __shared__ float sa[GEMM_ROWS][GEMM_STEP + 1];
-    __shared__ float sb[HALVES][GEMM_STEP][GEMM_COLS];
-    __shared__ Tile tile;
-    wait_prior_grid();
-    if (threadIdx.x == 0)
-        tile = find_tile(offsets, E, N, GEMM_ROWS, blockIdx.y, blockIdx.x == 0 ? err_word : nullptr);
-    __syncthreads();
-    if (tile.rows == 0)
-        return;
-    const int kb = K / 128, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int wide = OUT == OUT_SWIGLU ? 2 * M : M;
-    const int ob = (wide + 127) / 128;
-    const int o0 = blockIdx.x * GEMM_COLS;
-    const int64_t wbase = (int64_t)tile.expert * wide * K;
-    float acc[HALVES][4][4] = {}, part[HALVES][4][4];
-    for (int b = 0; b < kb; b++) {
-        for (int h = 0; h < HALVES; h++)
-            for (int i = 0; i < 4; i++)
-                for (int j = 0; j < 4; j++)
-                    part[h][i][j] = 0.0f;
-        for (int k0 = b * 128; k0 < (b + 1) * 128; k0 += GEMM_STEP) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < GEMM_ROWS * GEMM_STEP; i += GEMM_THREADS) {
-                const int r = i / GEMM_STEP, c = i % GEMM_STEP;
-                sa[r][c] = r < tile.rows ? e4m3(a_q[(int64_t)(tile.row + r) * K + k0 + c]) : 0.0f;
-            }
-            for (int h = 0; h < HALVES; h++)
-                for (int i = threadIdx.x; i < GEMM_COLS * GEMM_STEP; i += GEMM_THREADS) {
-                    const int c = TRANS ? i % GEMM_COLS : i / GEMM_STEP;
-                    const int r = TRANS ? i / GEMM_COLS : i % GEMM_STEP;
-                    const int o = o0 + c;
-                    const int64_t at = TRANS ? (int64_t)(k0 + r) * M + o
-                                             : (int64_t)(o + h * M) * K + k0 + r;
-                    sb[h][r][c] = o < M ? e4m3(w_q[wbase + at]) : 0.0f;
-                }
-            __syncthreads();
-            for (int c = 0; c < GEMM_STEP; c++)
-                for (int h = 0; h < HALVES; h++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-#pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            part[h][i][j] = fmaf(sa[ty * 4 + i][c], sb[h][c][tx + 32 * j],
-                                                 part[h][i][j]);
-        }
-        for (int h = 0; h < HALVES; h++) {
-            const int o = o0 / 128 + h * (M / 128);
-            const float ws = w_s[(int64_t)tile.expert * ob * kb +
-                                 (TRANS ? (int64_t)b * ob + o : (int64_t)o * kb + b)];
-            for (int i = 0; i < 4; i++) {
-                const int r = ty * 4 + i;
-                const float s = r < tile.rows ? a_s[(int64_t)(tile.row + r) * kb + b] * ws : 0.0f;
-                for (int j = 0; j < 4; j++)
-                    acc[h][i][j] = fmaf(part[h][i][j], s, acc[h][i][j]);
-            }
-        }
-    }
-    for (int i = 0; i < 4; i++) {
-        const int r = ty * 4 + i;
-        if (r >= tile.rows)  // uniform in the warp
-            continue;
-        const int64_t n = tile.row + r;
-        if constexpr (OUT == OUT_SWIGLU) {
-            float h[4], amax = 0.0f;
-            for (int j = 0; j < 4; j++) {
-                const float g = acc[0][i][j];
-                h[j] = g / (1.0f + expf(-g)) * acc[HALVES - 1][i][j];
-                amax = fmaxf(amax, fabsf(h[j]));
-            }
-            for (int d = 16; d > 0; d >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, d));
-            float scale = 1.0f, inv = 0.0f;
-            block_scale(amax, scale, inv);
-            for (int j = 0; j < 4; j++)
-                static_cast<uint8_t *>(out)[n * M + o0 + tx + 32 * j] =
-                    (uint8_t)__nv_cvt_float_to_fp8(__fmul_rn(h[j], inv), __NV_SATFINITE, __NV_E4M3);
-            if (tx == 0)
-                out_s[n * (M / 128) + o0 / 128] = scale;
-        } else {
-            for (int j = 0; j < 4; j++) {
-                const int o = o0 + tx + 32 * j;
-                if (o >= M)
-                    continue;
-                if constexpr (OUT == OUT_ROWS_F32)
-                    static_cast<float *>(out)[n * M + o] = acc[0][i][j];
-                else
-                    static_cast<__nv_bfloat16 *>(out)[n * M + o] = __float2bfloat16_rn(acc[0][i][j]);
-            }
-        }
-    }
+    auto *kernel = expert_gemm_kernel<OUT, TRANS>;
+    cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)G_SMEM);
+    if (st != cudaSuccess)
+        return st;
+    const int64_t wide = OUT == OUT_SWIGLU ? 2 * (int64_t)g.M : g.M;
+    CUtensorMap map_a, map_w;
+    st = encode_map(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a_q, 1, g.N, K, G_BOX, 128);
+    if (st != cudaSuccess)
+        return st;
+    st = encode_map(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q, g.E, TRANS ? K : wide,
+                    TRANS ? wide : K, 128, 128);
+    if (st != cudaSuccess)
+        return st;
+    // no more CTAs than tiles can be (each expert may add one partial row tile)
+    const int64_t most = ((int64_t)g.N / G_ROWS + (g.E < g.N ? g.E : g.N)) * g.col_tiles;
+    const int grid = (int)(most < sm_count() ? most : sm_count());
+    return launch_pdl(kernel, dim3(grid), dim3(G_THREADS), G_SMEM, stream, map_a, map_w, g);
 }
 
 }  // namespace
@@ -142,13 +371,13 @@ cudaError_t launch_expert_gemm(int N, int K, int M, int E, const uint8_t *a_q, c
 {
     if (N == 0)
         return cudaSuccess;
-    const dim3 grid((M + GEMM_COLS - 1) / GEMM_COLS, (N + GEMM_ROWS - 1) / GEMM_ROWS + E);
-    auto *kernel = transpose_w ? (out_f32 ? expert_gemm_kernel<OUT_ROWS_F32, true>
-                                          : expert_gemm_kernel<OUT_ROWS_BF16, true>)
-                               : (out_f32 ? expert_gemm_kernel<OUT_ROWS_F32, false>
-                                          : expert_gemm_kernel<OUT_ROWS_BF16, false>);
-    return launch_pdl(kernel, grid, dim3(GEMM_THREADS), 0, stream, N, K, M, E, a_q, a_s, offsets,
-                      w_q, w_s, out, (float *)nullptr, err_word);
+    const GemmArgs g = {N,   K / 128, M, E, (M + G_COLS - 1) / G_COLS, a_s, w_s, offsets, out,
+                        nullptr, err_word};
+    if (transpose_w)
+        return out_f32 ? run_gemm<OUT_F32, true>(g, K, a_q, w_q, stream)
+                       : run_gemm<OUT_BF16, true>(g, K, a_q, w_q, stream);
+    return out_f32 ? run_gemm<OUT_F32, false>(g, K, a_q, w_q, stream)
+                   : run_gemm<OUT_BF16, false>(g, K, a_q, w_q, stream);
 }
 
 cudaError_t launch_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q, const float *a_s,
@@ -157,9 +386,8 @@ cudaError_t launch_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q,
 {
     if (N == 0)
         return cudaSuccess;
-    const dim3 grid(I / GEMM_COLS, (N + GEMM_ROWS - 1) / GEMM_ROWS + E);
-    return launch_pdl(expert_gemm_kernel<OUT_SWIGLU, false>, grid, dim3(GEMM_THREADS), 0, stream, N,
-                      K, I, E, a_q, a_s, offsets, w_q, w_s, (void *)h_q, h_s, err_word);
+    const GemmArgs g = {N, K / 128, I, E, I / 128, a_s, w_s, offsets, h_q, h_s, err_word};
+    return run_gemm<OUT_SWIGLU, false>(g, K, a_q, w_q, stream);
 }
 
 }  // namespace moe

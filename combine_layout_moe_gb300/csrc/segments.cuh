@@ -1,5 +1,5 @@
 // The experts' row segments, as the products' kernels cut them into tiles, and
-// the block quantisation that the products' epilogues share.
+// the block quantisation of the products' epilogues.
 #pragma once
 
 #include "common.cuh"
@@ -18,28 +18,59 @@ __device__ __forceinline__ int2 segment(const int32_t *offsets, int e, int N, ui
     return make_int2(lo, hi);
 }
 
-struct Tile {
-    int expert, row, rows;
+// Every expert's first row, and the running count of row tiles before it.
+struct Segments {
+    int lo[MOE_MAX_EXPERTS], hi[MOE_MAX_EXPERTS];
+    int first[MOE_MAX_EXPERTS + 1];
 };
 
-// The `index`-th tile of `step` rows, the experts' segments one after another;
-// rows == 0 behind the last.
-__device__ inline Tile find_tile(const int32_t *offsets, int E, int N, int step, int index,
-                                 uint32_t *err_word)
+// Fills s, in shared memory, for tiles of `step` rows; called by the whole CTA,
+// complete when it returns.  err_word: of one CTA, so that a fault is reported
+// once.
+__device__ inline void load_segments(Segments &s, const int32_t *offsets, int E, int N, int step,
+                                     uint32_t *err_word)
 {
-    Tile t = {0, 0, 0};
-    for (int e = 0; e < E; e++) {
-        const int2 s = segment(offsets, e, N, err_word);
-        const int tiles = (s.y - s.x + step - 1) / step;
-        if (index < tiles) {
-            t.expert = e;
-            t.row = s.x + index * step;
-            t.rows = min(step, s.y - t.row);
-            return t;
-        }
-        index -= tiles;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const int2 r = segment(offsets, e, N, err_word);
+        s.lo[e] = r.x;
+        s.hi[e] = r.y;
     }
-    return t;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const int tiles = e < E ? (s.hi[e] - s.lo[e] + step - 1) / step : 0;
+            int sum = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(FULL_MASK, sum, d);
+                if (lane >= d)
+                    sum += v;
+            }
+            if (e < E)
+                s.first[e] = before + sum - tiles;
+            before += __shfl_sync(FULL_MASK, sum, 31);
+        }
+        if (lane == 0)
+            s.first[E] = before;
+    }
+    __syncthreads();
+}
+
+// The expert whose row tiles hold number m (m < s.first[E]).
+__device__ __forceinline__ int expert_of_tile(const Segments &s, int E, int m)
+{
+    int lo = 0, hi = E;  // first[lo] <= m < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.first[mid] <= m)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
 }
 
 // Scale and reciprocal of a block whose largest magnitude is amax, each one

@@ -1,0 +1,16 @@
+// Host side of the tensor copies: encoding a tensor map.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+// A map of a dense row-major [planes, rows, cols] array in boxes of box_rows x
+// box_cols (box_cols elements span at most 128 bytes), 128-byte swizzle, zeros
+// outside.  Rows are cols * element size bytes, a multiple of 16.
+cudaError_t encode_map(CUtensorMap *map, CUtensorMapDataType type, int element, const void *base,
+                       int64_t planes, int64_t rows, int64_t cols, int box_rows, int box_cols);
+
+}  // namespace moe
