@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-        if (lane == 0) {
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
@@ -129,20 +128,23 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 const int c0 = OUT == OUT_SWIGLU ? t.col * 128 : t.col * G_COLS;
                 const int c1 = OUT == OUT_SWIGLU ? g.M + c0 : c0 + 128;
                 for (int b = 0; b < g.kb; b++) {
-                    if (!(ok = mbar_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
+                    if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
                     const uint32_t bar = smem_addr(&sh.full[s]);
                     const uint32_t at = smem_addr(stages + s * G_STAGE);
-                    mbar_arrive_expect_tx(bar, boxes * G_BOX * 128 + 2 * G_B_HALF);
-                    for (int i = 0; i < boxes; i++)
-                        tensor_g2s(at + i * G_BOX * 128, &map_a, b * 128, t.row + i * G_BOX, 0,
-                                   bar);
-                    if (TRANS) {
-                        tensor_g2s(at + G_A_BYTES, &map_w, c0, b * 128, t.expert, bar);
-                        tensor_g2s(at + G_A_BYTES + G_B_HALF, &map_w, c1, b * 128, t.expert, bar);
-                    } else {
-                        tensor_g2s(at + G_A_BYTES, &map_w, b * 128, c0, t.expert, bar);
-                        tensor_g2s(at + G_A_BYTES + G_B_HALF, &map_w, b * 128, c1, t.expert, bar);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, boxes * G_BOX * 128 + 2 * G_B_HALF);
+                        for (int i = 0; i < boxes; i++)
+                            tensor_g2s(at + i * G_BOX * 128, &map_a, b * 128, t.row + i * G_BOX,
+                                       0, bar);
+                        const uint32_t wt = at + G_A_BYTES;
+                        if (TRANS) {
+                            tensor_g2s(wt, &map_w, c0, b * 128, t.expert, bar);
+                            tensor_g2s(wt + G_B_HALF, &map_w, c1, b * 128, t.expert, bar);
+                        } else {
+                            tensor_g2s(wt, &map_w, b * 128, c0, t.expert, bar);
+                            tensor_g2s(wt + G_B_HALF, &map_w, b * 128, c1, t.expert, bar);
+                        }
                     }
                     issued++;
                     if (++s == G_STAGES) {
@@ -153,34 +155,34 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
             // copies still in flight land before the CTA may end
             for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
-                ok = mbar_wait(smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
-        }
-    }
-    if (warp == 9) {
-        if (lane == 0) {
+                ok = warp_wait(smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+        } else if (warp == 9) {
             constexpr uint32_t idesc = mma_desc(G_ROWS, G_COLS, 0, false, TRANS);
+            const uint32_t base = smem_addr(stages);
+            // rows of 128 inputs: the next 32 are 32 bytes on.  Outputs contiguous:
+            // 32 rows of 128 bytes on
+            constexpr uint32_t b_step = (TRANS ? 4096 : 32) >> 4, a_step = 32 >> 4;
+            const uint64_t a0 = smem_desc(base, 16, 1024);
+            const uint64_t b0 = smem_desc(base + G_A_BYTES, TRANS ? G_B_HALF : 16, 1024);
             int s = 0, d = 0;
             uint32_t phase = 0, d_phase = 0;
             int64_t issued = 0;
             for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
                 for (int b = 0; b < g.kb; b++) {
-                    if (!(ok = mbar_wait(smem_addr(&sh.sums_empty[d]), d_phase ^ 1) &&
-                               mbar_wait(smem_addr(&sh.full[s]), phase)))
+                    if (!(ok = warp_wait2(smem_addr(&sh.sums_empty[d]), d_phase ^ 1,
+                                          smem_addr(&sh.full[s]), phase)))
                         break;
                     tcgen05_after_sync();
-                    const uint32_t at = smem_addr(stages + s * G_STAGE);
+                    const uint64_t da = a0 + (uint32_t)(s * (G_STAGE >> 4));
+                    const uint64_t db = b0 + (uint32_t)(s * (G_STAGE >> 4));
+                    const uint32_t to = tmem + d * G_COLS;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        // rows of 128 inputs: the next 32 are 32 bytes on.  Outputs
-                        // contiguous: 32 rows of 128 bytes on
-                        const uint64_t da = smem_desc(at + i * 32, 16, 1024);
-                        const uint64_t db =
-                            TRANS ? smem_desc(at + G_A_BYTES + i * 4096, G_B_HALF, 1024)
-                                  : smem_desc(at + G_A_BYTES + i * 32, 16, 1024);
-                        mma_f8(tmem + d * G_COLS, da, db, idesc, i > 0);
+                        for (int i = 0; i < 4; i++)
+                            mma_f8(to, da + i * a_step, db + i * b_step, idesc, i > 0);
+                        tcgen05_commit(smem_addr(&sh.sums_full[d]));
+                        tcgen05_commit(smem_addr(&sh.empty[s]));
                     }
-                    tcgen05_commit(smem_addr(&sh.empty[s]));
-                    tcgen05_commit(smem_addr(&sh.sums_full[d]));
                     issued++;
                     if (++s == G_STAGES) {
                         s = 0;
@@ -194,42 +196,85 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
             // and so do the MMAs' arrivals
             for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
-                ok = mbar_wait(smem_addr(&sh.empty[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+                ok = warp_wait(smem_addr(&sh.empty[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
         const int ob = (g.M + 127) / 128;  // 128-output blocks of the weights' scales
+        const int blocks = OUT == OUT_SWIGLU ? 2 * ob : ob;
+        const bool quads = g.kb % 4 == 0;  // rows of scales start on 16 bytes
+        // The scales of a tile: this thread's row, four blocks ahead of their use,
+        // and the two halves' weights, 32 blocks at a time, one a lane.
+        const float *sa = nullptr, *w0 = nullptr, *w1 = nullptr;
+        const int64_t wstep = TRANS ? blocks : 1;
+        float s_row[4], s_w0 = 0.0f, s_w1 = 0.0f;
+        auto load_rows = [&](int b) {
+            if (quads) {
+                const float4 v = *reinterpret_cast<const float4 *>(sa + b);
+                s_row[0] = v.x;
+                s_row[1] = v.y;
+                s_row[2] = v.z;
+                s_row[3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    s_row[i] = sa[min(b + i, g.kb - 1)];
+            }
+        };
+        auto load_weights = [&](int b) {
+            const int at = min(b + lane, g.kb - 1);
+            s_w0 = w0[at * wstep];
+            s_w1 = w1[at * wstep];
+        };
+        auto open_tile = [&](const GemmTile &t) {
+            sa = g.a_s + (int64_t)(t.row + min(r, t.rows - 1)) * g.kb;
+            const int o0 = OUT == OUT_SWIGLU ? t.col : 2 * t.col;
+            const int o1 = OUT == OUT_SWIGLU ? ob + t.col : min(o0 + 1, ob - 1);
+            const float *sw = g.w_s + (int64_t)t.expert * blocks * g.kb;
+            w0 = sw + (TRANS ? o0 : (int64_t)o0 * g.kb);
+            w1 = sw + (TRANS ? o1 : (int64_t)o1 * g.kb);
+            load_rows(0);
+            load_weights(0);
+        };
         int d = 0;
         uint32_t d_phase = 0;
+        GemmTile next;
+        if (blockIdx.x < tiles) {
+            next = gemm_tile(sh.seg, g, blockIdx.x);
+            open_tile(next);
+        }
         for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-            const GemmTile t = gemm_tile(sh.seg, g, tile);
+            const GemmTile t = next;
             const bool busy = quarter * 32 < t.rows;  // of the warp
-            const float *sa = g.a_s + (int64_t)(t.row + min(r, t.rows - 1)) * g.kb;
-            const int o0 = OUT == OUT_SWIGLU ? t.col : 2 * t.col;
-            const int o1 = OUT == OUT_SWIGLU ? g.M / 128 + t.col : min(o0 + 1, ob - 1);
-            const int blocks = OUT == OUT_SWIGLU ? 2 * ob : ob;
-            const float *sw = g.w_s + (int64_t)t.expert * blocks * g.kb;
-            const int64_t w0 = TRANS ? o0 : (int64_t)o0 * g.kb, w1 = TRANS ? o1 : (int64_t)o1 * g.kb;
-            const int64_t wstep = TRANS ? blocks : 1;
             float2 acc[2][32];
 #pragma unroll
             for (int i = 0; i < 32; i++)
                 acc[0][i] = acc[1][i] = make_float2(0.0f, 0.0f);
-            float s0 = 0.0f, s1 = 0.0f, sr = sa[0];
+            float c_row[4], c_w0 = 0.0f, c_w1 = 0.0f;
             for (int b = 0; b < g.kb; b++) {
-                if ((b & 31) == 0) {  // the weights' scales of the next 32 blocks, one a lane
-                    const int at = min(b + lane, g.kb - 1);
-                    s0 = sw[w0 + at * wstep];
-                    s1 = sw[w1 + at * wstep];
+                if ((b & 31) == 0) {
+                    c_w0 = s_w0;
+                    c_w1 = s_w1;
+                    if (b + 32 < g.kb)
+                        load_weights(b + 32);
                 }
-                const float f0 = sr * __shfl_sync(FULL_MASK, s0, b & 31);
-                const float f1 = sr * __shfl_sync(FULL_MASK, s1, b & 31);
-                sr = sa[min(b + 1, g.kb - 1)];
-                ok = __all_sync(FULL_MASK, mbar_wait(smem_addr(&sh.sums_full[d]), d_phase));
+                if ((b & 3) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        c_row[i] = s_row[i];
+                    if (b + 4 < g.kb)
+                        load_rows(b + 4);
+                }
+                const float sr = c_row[0];
+                c_row[0] = c_row[1];
+                c_row[1] = c_row[2];
+                c_row[2] = c_row[3];
+                const float f0 = sr * __shfl_sync(FULL_MASK, c_w0, b & 31);
+                const float f1 = sr * __shfl_sync(FULL_MASK, c_w1, b & 31);
+                ok = warp_wait(smem_addr(&sh.sums_full[d]), d_phase);
                 if (!ok)
                     break;
                 if (busy) {
@@ -260,6 +305,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
             if (!ok)
                 break;
+            if (tile + (int)gridDim.x < tiles) {  // its first scales load during the epilogue
+                next = gemm_tile(sh.seg, g, tile + gridDim.x);
+                open_tile(next);
+            }
             const int64_t n = t.row + r;
             if constexpr (OUT == OUT_SWIGLU) {
                 float amax = 0.0f;

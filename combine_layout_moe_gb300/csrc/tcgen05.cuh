@@ -53,6 +53,19 @@ __device__ __forceinline__ void tcgen05_after_sync()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp, the same at every call.  The loops around copies
+// and MMAs run with the whole warp, so that addresses and descriptors stay in
+// uniform registers, and only the instruction itself is the elected lane's: a
+// loop under `lane == 0` took some 1000 cycles for a block's four MMAs.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Arrives on `bar` when every MMA this thread issued so far has completed.
 __device__ __forceinline__ void tcgen05_commit(uint32_t bar)
 {

@@ -75,6 +75,41 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
+// The same for waits of a few hundred cycles that follow each other closely:
+// the timer, whose reading takes longer than such a wait, is looked at once in
+// 256 tries only.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 256; i++)
+            if (mbar_try_wait(bar, parity))
+                return true;
+        const uint64_t t = global_ns();
+        if (t0 == 0)
+            t0 = t;
+        else if (t - t0 > MBAR_TIMEOUT_NS)
+            return false;
+    }
+}
+
+// The same for a whole warp, whose lanes agree on the answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
+}
+
+// For two barriers; the answers of both first tries are awaited together.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b,
+                                           uint32_t parity_b)
+{
+    const bool a = mbar_try_wait(bar_a, parity_a), b = mbar_try_wait(bar_b, parity_b);
+    if (__all_sync(0xffffffffu, a && b))
+        return true;
+    return warp_wait(bar_a, parity_a) && warp_wait(bar_b, parity_b);
+}
+
 // Global -> shared bulk copy of `bytes` (multiple of 16, both addresses
 // 16-byte aligned); completion is counted on mbarrier `bar` as transaction bytes.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes,
