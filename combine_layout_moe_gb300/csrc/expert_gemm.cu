@@ -47,8 +47,9 @@ constexpr int G_STAGE = G_A_BYTES + 2 * G_B_HALF;
 struct GemmShared {
     uint64_t full[G_STAGES], empty[G_STAGES];
     uint64_t sums_full[2], sums_empty[2];
+    uint64_t amax_full[4];  // the two warps of 32 rows have written theirs
     uint32_t tmem;
-    float amax[2][G_ROWS];
+    float amax[2][2][G_ROWS];  // of two tiles in turn
     Segments seg;
 };
 
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             mbar_init(smem_addr(&sh.sums_full[i]), 1);
             mbar_init(smem_addr(&sh.sums_empty[i]), G_PROMOTE / 32);
         }
+        for (int i = 0; i < 4; i++)
+            mbar_init(smem_addr(&sh.amax_full[i]), 2);
         mbar_fence_init();
         prefetch_map(&map_a);
         prefetch_map(&map_w);
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             load_weights(0);
         };
         int d = 0;
-        uint32_t d_phase = 0;
+        uint32_t d_phase = 0, turn = 0;
         GemmTile next;
         if (blockIdx.x < tiles) {
             next = gemm_tile(sh.seg, g, blockIdx.x);
@@ -320,10 +323,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     amax = fmaxf(amax, fmaxf(fabsf(acc[0][i].x), fabsf(acc[0][i].y)));
                 }
                 // the block's other 64 channels are with the warp four on
-                sh.amax[half][r] = amax;
-                named_barrier(1 + quarter, 64);
-                amax = fmaxf(amax, sh.amax[half ^ 1][r]);
-                named_barrier(1 + quarter, 64);
+                sh.amax[turn][half][r] = amax;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.amax_full[quarter]));
+                if (!(ok = warp_wait(smem_addr(&sh.amax_full[quarter]), turn)))
+                    break;
+                amax = fmaxf(amax, sh.amax[turn][half ^ 1][r]);
+                turn ^= 1;
                 if (r < t.rows) {
                     float scale, inv;
                     block_scale(amax, scale, inv);

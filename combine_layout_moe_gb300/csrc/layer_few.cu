@@ -63,6 +63,7 @@ struct FewShared {
     uint8_t token[MOE_FEW_MAX_PAIRS];      // token of each row
     int16_t pos[MOE_MAX_EXPERTS];          // place of e in act
     int active, longest, last;
+    int failed;                            // a wait gave up
 };
 
 // Weights in boxes of 1, 2, 4 and 8 tiles' rows (UP: of one half, gate or up).
@@ -171,6 +172,7 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
             longest = max(longest, (int)__reduce_max_sync(FULL_MASK, (unsigned)mine));
         }
         if (lane == 0) {
+            s.failed = 0;
             s.row0[n] = rows;
             s.active = n;
             s.longest = longest;
@@ -308,11 +310,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
     // rows of a stage's activations: all tokens of x, or the most that an expert has
     const int act_rows = DOWN ? 16 << box_of(sh.longest) : (g.T + 7) & ~7;
-    const int stage_bytes = FEW_W_BYTES + TY::WIDTH * act_rows * 128;
+    const Work whole = few_work<DOWN>(sh, g);
     const uint8_t *ring_end = DOWN ? reinterpret_cast<uint8_t *>(sums)
                                    : top - sizeof(FewShared);
-    const int stages = min((int)((ring_end - ring) / stage_bytes), FEW_MAX_STAGES);
-    const Work whole = few_work<DOWN>(sh, g);
+    const int ring_bytes = (int)(ring_end - ring);
+    // DOWN: a CTA of few tiles splits the inputs over its warps as well, `slices`
+    // blocks a stage (as long as four stages fit); the slices' sums meet at the end
+    const int slice_w = DOWN ? whole.per * FEW_TILE : FEW_W_BYTES;
+    const int slice_bytes = slice_w + TY::WIDTH * act_rows * 128;
+    const int slices =
+        DOWN ? max(min(FEW_WARPS / whole.per, ring_bytes / (4 * slice_bytes)), 1) : 1;
+    const int stage_bytes = slices * slice_bytes;
+    // at least three: a slice is 48 KB at most, and the ring has 170
+    const int stages = min(ring_bytes / stage_bytes, FEW_MAX_STAGES);
     const int row_tiles = (g.H + 15) / 16;
     const int groups = DOWN ? (row_tiles + whole.per - 1) / whole.per : 0;
     const int rounds = DOWN ? groups * whole.shares : (int)gridDim.x;
@@ -340,29 +350,34 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 const int row = DOWN ? 2 * row0 : 0;
                 const CUtensorMap *act = &maps.act[DOWN ? box : 0];
                 const int wrow = p.tile * (DOWN ? 16 : 8);
-                for (int b = 0; b < blocks; b++) {
+                for (int b0 = 0; b0 < blocks; b0 += slices) {
                     if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
                     const uint32_t bar = smem_addr(&sh.full[s]);
-                    const uint32_t at = smem_addr(ring) + s * stage_bytes;
+                    uint32_t at = smem_addr(ring) + s * stage_bytes;
+                    const int end = min(b0 + slices, blocks);
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, p.tiles * FEW_TILE + TY::WIDTH * rows * 128);
-                        int done = 0;  // tiles, in boxes of falling size
+                        mbar_arrive_expect_tx(
+                            bar, (end - b0) * (p.tiles * FEW_TILE + TY::WIDTH * rows * 128));
+                        for (int b = b0; b < end; b++, at += slice_bytes) {
+                            int done = 0;  // tiles, in boxes of falling size
 #pragma unroll
-                        for (int i = 3; i >= 0; i--) {
-                            if (!(p.tiles >> i & 1))
-                                continue;
-                            const int r = wrow + done * (DOWN ? 16 : 8);
-                            tensor_g2s(at + done * TILE_STEP, &maps.w[i], b * TY::KB, r, e, bar);
-                            if (!DOWN)
-                                tensor_g2s(at + HALF_STEP + done * TILE_STEP, &maps.w[i],
-                                           b * TY::KB, g.I + r, e, bar);
-                            done += 1 << i;
+                            for (int i = 3; i >= 0; i--) {
+                                if (!(p.tiles >> i & 1))
+                                    continue;
+                                const int r = wrow + done * (DOWN ? 16 : 8);
+                                tensor_g2s(at + done * TILE_STEP, &maps.w[i], b * TY::KB, r, e,
+                                           bar);
+                                if (!DOWN)
+                                    tensor_g2s(at + HALF_STEP + done * TILE_STEP, &maps.w[i],
+                                               b * TY::KB, g.I + r, e, bar);
+                                done += 1 << i;
+                            }
+#pragma unroll
+                            for (int i = 0; i < TY::WIDTH; i++)
+                                tensor_g2s(at + slice_w + i * act_rows * 128, act,
+                                           b * TY::KB + i * 64, row, 0, bar);
                         }
-#pragma unroll
-                        for (int i = 0; i < TY::WIDTH; i++)
-                            tensor_g2s(at + FEW_W_BYTES + i * act_rows * 128, act,
-                                       b * TY::KB + i * 64, row, 0, bar);
                     }
                     issued++;
                     if (++s == stages) {
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
 
         if (DOWN) {
-            __syncwarp();
+            named_barrier(1, 32 * FEW_WARPS);  // the job before has been read
             for (int i = lane; i < 16 * g.T; i += 32)
                 sums[warp * 16 * g.T + i] = 0.0f;
             __syncwarp();
@@ -384,8 +399,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         while (ok && work.q < work.end) {
             const Pass p = next_pass<DOWN>(work);
             const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
-            const bool busy = warp < p.tiles;
-            const int tile = p.tile + warp;
+            const int slice = DOWN ? warp / whole.per : 0;
+            const int in_pass = DOWN ? warp - slice * whole.per : warp;
+            const bool busy = slice < slices && in_pass < p.tiles;
+            const int tile = p.tile + in_pass;
             const float *s_lo = nullptr, *s_hi = nullptr;  // of rows 0-7 and 8-15
             float v_lo = 0.0f, v_hi = 0.0f;
             if (FP8 && busy) {
@@ -410,17 +427,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 col_row[i] = DOWN ? 2 * col : col < n ? sh.token[row0 + col] : 0;
             }
             uint32_t nan_lo = 0, nan_hi = 0;
-            for (int b = 0; b < blocks; b++) {
-                if (FP8 && busy && (b & 31) == 0) {  // the next 32 blocks' scales, one a lane
-                    const int at = min(b + lane, blocks - 1);
+            for (int b0 = 0, mine = 0; b0 < blocks; b0 += slices, mine++) {
+                const int b = b0 + slice;
+                if (FP8 && busy && (mine & 31) == 0) {  // of the next 32 blocks, one a lane
+                    const int at = min(b + lane * slices, blocks - 1);
                     v_lo = s_lo[at];
                     v_hi = s_hi[at];
                 }
                 if (!(ok = warp_wait(smem_addr(&sh.full[s]), phase)))
                     break;
-                if (busy) {
-                    const uint32_t at = smem_addr(ring) + s * stage_bytes;
-                    const uint32_t wt = at + warp * TILE_STEP + ((lane >> 3) & 1) * HALF_STEP +
+                if (busy && b < blocks) {
+                    const uint32_t at =
+                        smem_addr(ring) + s * stage_bytes + slice * slice_bytes;
+                    const uint32_t wt = at + in_pass * TILE_STEP + ((lane >> 3) & 1) * HALF_STEP +
                                         (lane & 7) * 128;
                     uint32_t a[TY::STEPS][4];
 #pragma unroll
@@ -440,17 +459,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     }
                     float f_lo = 1.0f, f_hi = 1.0f;
                     if (FP8) {
-                        f_lo = __shfl_sync(FULL_MASK, v_lo, b & 31);
-                        f_hi = __shfl_sync(FULL_MASK, v_hi, b & 31);
+                        f_lo = __shfl_sync(FULL_MASK, v_lo, mine & 31);
+                        f_hi = __shfl_sync(FULL_MASK, v_hi, mine & 31);
                     }
 #pragma unroll
                     for (int grp = 0; grp < NG; grp++) {
                         if (grp * 8 < n) {
-                            float part[4] = {};
+                            float part[2 * TERMS][4] = {};  // sums that do not wait for each other
 #pragma unroll
                             for (int term = 0; term < TERMS; term++) {
                                 const uint32_t r = col_row[grp] + term;
-                                const uint32_t row = at + FEW_W_BYTES + r * 128;
+                                const uint32_t row = at + slice_w + r * 128;
                                 if constexpr (FP8) {
                                     const uint32_t in = (c4 & 1) * 8;
 #pragma unroll
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                                         const uint2 v = lds64(
                                             row + (j >> 2) * act_rows * 128 + in +
                                             ((((j & 3) * 2 + (c4 >> 1)) ^ (r & 7)) << 4));
-                                        mma16816(part, a[j], __byte_perm(v.x, v.y, 0x5410),
+                                        mma16816(part[2 * term + (j & 1)], a[j], __byte_perm(v.x, v.y, 0x5410),
                                                  __byte_perm(v.x, v.y, 0x7632));
                                     }
                                 } else {
@@ -466,15 +485,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                                     for (int j = 0; j < TY::STEPS; j += 2) {
                                         uint32_t v[4];
                                         ldsm4(row + (((j * 2 + (lane >> 3)) ^ (r & 7)) << 4), v);
-                                        mma16816(part, a[j], v[0], v[1]);
-                                        mma16816(part, a[j + 1], v[2], v[3]);
+                                        mma16816(part[2 * term], a[j], v[0], v[1]);
+                                        mma16816(part[2 * term + 1], a[j + 1], v[2], v[3]);
                                     }
                                 }
                             }
-                            acc[grp][0] = fmaf(part[0], f_lo, acc[grp][0]);
-                            acc[grp][1] = fmaf(part[1], f_lo, acc[grp][1]);
-                            acc[grp][2] = fmaf(part[2], f_hi, acc[grp][2]);
-                            acc[grp][3] = fmaf(part[3], f_hi, acc[grp][3]);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                float v = part[0][i] + part[1][i];
+                                if (DOWN)
+                                    v += part[2 * TERMS - 2][i] + part[2 * TERMS - 1][i];
+                                acc[grp][i] = fmaf(v, i < 2 ? f_lo : f_hi, acc[grp][i]);
+                            }
                         }
                     }
                 }
@@ -531,11 +553,22 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             }
         }
 
-        if (DOWN && ok) {
-            __syncwarp();
+        if (DOWN) {
+            if (!ok)
+                sh.failed = 1;
+            named_barrier(1, 32 * FEW_WARPS);  // every warp's sums are complete
+            if (sh.failed) {                   // and no warp waits for one that has left
+                ok = false;
+                continue;
+            }
+            // the slices of a tile, added up by its first warp
             const int o = (work.tile + warp) * 16 + (lane & 15);
             const bool mine = warp < work.tiles && o < g.H;
             float *tile_sums = sums + warp * 16 * g.T + (lane & 15);
+            if (mine)
+                for (int t = lane >> 4; t < g.T; t += 2)
+                    for (int i = 1; i < slices; i++)
+                        tile_sums[t * 16] += tile_sums[(i * whole.per * g.T + t) * 16];
             if (whole.shares > 1) {
                 const int64_t plane = (int64_t)g.T * g.H;
                 if (mine)
