@@ -5,21 +5,31 @@
 // w[t,e] the sum of token t's weights over the slots that name e.  With few rows
 // an expert the layer is a stream of weights: every chosen expert's are read
 // once, at the rate of the HBM, and what is computed on the way has to keep up
-// with it.  So a CTA's eight warps take 16 weight rows each (one mma tile), a
-// producer warp keeps a ring of 128-byte-wide weight boxes and the matching piece
-// of the activations in flight, and each warp multiplies its tile with all of the
-// expert's tokens (mma.sync, tokens as columns in groups of eight).  The tile's
-// sums stay in its warp: no exchange inside a product.  A tcgen05.mma would take
-// at least 64 rows a tile and FP8 activations to match FP8 weights; here they stay
-// bf16, and E4M3 weights widen to bf16 in registers (exactly).
+// with it.  A producer warp keeps a ring of stages in flight, two 128-byte-wide
+// blocks of the inputs each, in as few tensor copies as can be (issuing one takes
+// the warp some 100 cycles).  Three feeder warps run ahead beside it and put the
+// matching pieces of the entry's tokens into the stage.  A consumer warp takes 16
+// weight rows (one mma tile) of its slice of the blocks and multiplies them with all
+// of the tokens (mma.sync, tokens as columns in groups of eight; an expert of more
+// than 32 tokens counts as two entries).  A tcgen05.mma would take at least 64 rows a
+// tile, and FP8 activations to match FP8 weights; here activations keep their
+// precision:
+//   bf16 weights  x as it is, h as two bf16 terms
+//   E4M3 weights  widen to fp16 (exactly, one instruction for two codes); x goes in
+//                 as fp16, h as two fp16 terms, times a power of two for each token
+//                 and 128 inputs that brings the largest to 2^14 and is taken back
+//                 with the weights' scale.  What is below 2^-39 of its block's
+//                 largest is lost
 //
 // First kernel (UP): a tile is 8 gate rows and the 8 up rows of the same channels,
-// so SwiGLU is a lane's own; h, weighted, goes to the workspace as two bf16 terms.
-// The (expert, channel) range is cut evenly over the CTAs.  Second (DOWN): a tile
-// is 16 output rows; a CTA takes up to eight tiles for a share of the experts and
-// adds the experts up in shared memory, warp by warp; where experts are shared out,
-// the last CTA of a group of rows adds the shares in a fixed order.
+// so SwiGLU is a lane's own; h, weighted, goes to the workspace.  The (expert,
+// channel) range is cut evenly over the CTAs, whose warps are eight tiles x two
+// slices of the inputs.  Second (DOWN): a tile is 16 output rows; a CTA takes up to
+// eight tiles, as many pairs of slices as its warps allow, and a share of the experts, which
+// it adds up in shared memory; where experts are shared out, the last CTA of a group
+// of rows adds the shares in a fixed order.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "launch.h"
@@ -30,59 +40,63 @@ namespace moe {
 
 namespace {
 
-constexpr int FEW_WARPS = 8;  // consumers
-constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1);
+constexpr int FEW_WARPS = 16;   // consumers
+constexpr int FEW_TILES = 8;    // most tiles of a stage
+constexpr int FEW_FEEDERS = 3;  // warps that bring the activations
+constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1 + FEW_FEEDERS);
 constexpr int FEW_MAX_STAGES = 16;
-constexpr int FEW_TILE = 2048;  // 16 rows x 128 bytes
-constexpr int FEW_W_BYTES = FEW_WARPS * FEW_TILE;
-constexpr int FEW_MAX_SPLIT = 8;  // CTAs that may share the experts of a row group
+constexpr int FEW_ROWS = 32;      // most tokens of an entry
+constexpr int FEW_TILE = 2048;     // 16 rows x 128 bytes
+constexpr int FEW_FACTORS = 1024;  // of a stage: a power of two for each token and block
+constexpr int FEW_MAX_SPLIT = 8;   // CTAs that may share the experts of a row group
 constexpr size_t FEW_SMEM = 227 * 1024;
 
 template <typename W>
 struct FewType;
 template <>
 struct FewType<uint8_t> {
-    static constexpr int KB = 128;   // inputs of a stage: 128 bytes of a weight row
+    static constexpr int KB = 128;   // inputs of a block: 128 bytes of a weight row
     static constexpr int STEPS = 8;  // of K = 16
-    static constexpr int WIDTH = 2;  // 128-byte pieces of an activation row
+    using Act = __half;
 };
 template <>
 struct FewType<__nv_bfloat16> {
     static constexpr int KB = 64;
     static constexpr int STEPS = 4;
-    static constexpr int WIDTH = 1;
+    using Act = __nv_bfloat16;
 };
 
 struct FewShared {
-    uint64_t full[FEW_MAX_STAGES], empty[FEW_MAX_STAGES];
+    uint64_t full[FEW_MAX_STAGES], ready[FEW_MAX_STAGES], empty[FEW_MAX_STAGES];
+    uint64_t given[FEW_TILES], taken[FEW_TILES];  // UP: a tile's sums of the second slice
     uint32_t tokens[2][MOE_MAX_EXPERTS];   // bit t: expert e is named by token t
     int ids[MOE_FEW_MAX_PAIRS];            // topk_idx
-    int act[MOE_FEW_MAX_PAIRS];            // experts in use, by id
-    int row0[MOE_FEW_MAX_PAIRS + 1];       // first row of each in h
+    int act[MOE_FEW_MAX_PAIRS];            // entries: experts in use, by id
+    int row0[MOE_FEW_MAX_PAIRS + 1];       // first row of each in h, at most 32 an entry
     float w[MOE_FEW_MAX_PAIRS];            // weight of each row
     uint8_t token[MOE_FEW_MAX_PAIRS];      // token of each row
-    int16_t pos[MOE_MAX_EXPERTS];          // place of e in act
+    int16_t pos[MOE_MAX_EXPERTS];          // first entry of e
     int active, longest, last;
     int failed;                            // a wait gave up
 };
 
-// Weights in boxes of 1, 2, 4 and 8 tiles' rows (UP: of one half, gate or up).
-// Activations, UP: all T rows of x in act[0]; DOWN: 8, 16, 32 or 64 rows of h,
-// both terms.
+// Weights in boxes of 1, 2, 4 and 8 tiles' rows and two blocks.  Five dimensions: 128
+// bytes of a row, rows, the halves (gate and up; 1 for DOWN), blocks, experts.  Where a
+// row is not a whole number of blocks, the first is the whole row and a box one block.
 struct FewMaps {
-    CUtensorMap w[4], act[4];
+    CUtensorMap w[4];
 };
 
 struct FewArgs {
     int T, k, H, I, E;
-    const __nv_bfloat16 *x;  // UP: activations
-    __nv_bfloat16 *h;        // [row][two terms][I]
+    const __nv_bfloat16 *x;
+    float *h;  // [row][I]
     const int32_t *idx;
     const float *topk_w;
     const float *scales;
-    float *parts;            // DOWN: [split][T][H]
-    uint32_t *arrived;       // DOWN: per row group
-    int groups;              // of `arrived`, that UP clears
+    float *parts;       // DOWN: [split][T][H]
+    uint32_t *arrived;  // DOWN: per row group
+    int groups;         // of `arrived`, that UP clears
     void *out;
     bool out_f32;
     uint32_t *err_word;
@@ -102,8 +116,29 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1)
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_16816(__nv_bfloat16, float (&c)[4], const uint32_t (&a)[4],
+                                          uint32_t b0, uint32_t b1)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
@@ -112,18 +147,61 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Bytes 0 and 2, and bytes 1 and 3, of four E4M3 codes as bf16 pairs, exactly: the
-// code's exponent and mantissa fields at the foot of bf16's exponent, then times
-// 2^120, the difference of the biases (which also normalises subnormals).  The
-// two NaN codes come out as 480; `seen` gathers them in its bytes' top bits.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &even, uint32_t &odd, uint32_t &seen)
+__device__ __forceinline__ void mma_16816(__half, float (&c)[4], const uint32_t (&a)[4],
+                                          uint32_t b0, uint32_t b1)
 {
-    constexpr uint32_t S = 0x80008000u, F = 0x07f007f0u;
-    const uint32_t up = 0x7b807b80u;  // 2^120 twice
-    const uint32_t e = ((w << 8) & S) | ((w << 4) & F), o = (w & S) | ((w >> 4) & F);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(up));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(up));
-    seen |= (w & 0x7f7f7f7fu) + 0x01010101u;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes as two fp16 pairs.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &first, uint32_t &second)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(first), "=r"(second)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pair_bits(__half, float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pair_bits(__nv_bfloat16, float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 pair_values(__half, uint32_t bits)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&bits));
+}
+
+__device__ __forceinline__ float2 pair_values(__nv_bfloat16, uint32_t bits)
+{
+    return make_float2(bf16lo(bits), bf16hi(bits));
+}
+
+// What is left of v behind its first term; nothing behind an infinite one.
+__device__ __forceinline__ float rest_of(float v, float first)
+{
+    return fabsf(first) < __int_as_float(0x7f800000) ? v - first : 0.0f;
+}
+
+// The power of two that brings values of magnitude `top` (a block's largest, as
+// bits) to [2^14, 2^15), and its inverse; 1 where top is infinite or NaN.
+__device__ __forceinline__ float to_half_range(uint32_t top, float &inverse)
+{
+    const int e = (int)(top >> 23);
+    const int by = e == 255 ? 0 : min(141 - e, 126);
+    inverse = __int_as_float((127 - by) << 23);
+    return __int_as_float((127 + by) << 23);
 }
 
 // Who names whom, in shared memory; called by the whole CTA.
@@ -151,26 +229,29 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
         for (int e0 = 0; e0 < g.E; e0 += 32) {
             const int e = e0 + lane;
             const int mine = e < g.E ? __popc(s.tokens[0][e]) + __popc(s.tokens[1][e]) : 0;
-            const unsigned used = __ballot_sync(FULL_MASK, mine > 0);
-            if (used == 0)
+            if (!__any_sync(FULL_MASK, mine > 0))
                 continue;
-            int sum = mine;
+            const int entries = (mine + FEW_ROWS - 1) / FEW_ROWS;
+            int sum = mine | entries << 16;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(FULL_MASK, sum, d);
                 if (lane >= d)
                     sum += v;
             }
-            if (mine > 0) {
-                const int at = n + __popc(used & lanemask_lt());
-                s.act[at] = e;
-                s.pos[e] = (int16_t)at;
-                s.row0[at] = rows + sum - mine;
+            const int at = n + (sum >> 16) - entries, row = rows + (sum & 0xffff) - mine;
+            for (int i = 0; i < entries; i++) {
+                s.act[at + i] = e;
+                s.row0[at + i] = row + i * FEW_ROWS;
             }
-            n += __popc(used);
-            rows += __shfl_sync(FULL_MASK, sum, 31);
+            if (entries > 0)
+                s.pos[e] = (int16_t)at;
+            const int all = __shfl_sync(FULL_MASK, sum, 31);
+            n += all >> 16;
+            rows += all & 0xffff;
             longest = max(longest, (int)__reduce_max_sync(FULL_MASK, (unsigned)mine));
         }
+        longest = min(longest, FEW_ROWS);
         if (lane == 0) {
             s.failed = 0;
             s.row0[n] = rows;
@@ -204,10 +285,7 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
     __syncthreads();
 }
 
-// The smallest of 8, 16, 32, 64 (0 .. 3) that holds n.
-__device__ __forceinline__ int box_of(int n) { return n <= 8 ? 0 : n <= 16 ? 1 : n <= 32 ? 2 : 3; }
-
-// A stretch of work: up to eight tiles of one expert, over all of its inputs.
+// A stretch of work: up to eight tiles of one entry, over all of its inputs.
 struct Pass {
     int a, tile, tiles;
 };
@@ -231,19 +309,19 @@ __device__ Work few_work(const FewShared &s, const FewArgs &g)
         w.end = all * (b + 1) / grid;
         return w;
     }
-    // tiles a CTA takes, and shares of the experts: the fewest bytes for the
-    // busiest CTA, and then the fewest shares
+    // tiles a CTA takes, and shares of the experts: the fewest bytes for the busiest
+    // CTA; of equals the most tiles, whose stages are the largest
     const int all = (g.H + 15) / 16, experts = max(s.active, 1);
     int best = 0, shares = 1, cost = 0x7fffffff;
-    for (int n = 1; n <= FEW_WARPS; n++) {
+    for (int n = 1; n <= FEW_TILES; n++) {
         const int groups = (all + n - 1) / n;
-        const int sh = min(min(grid / groups, experts), FEW_MAX_SPLIT);
-        const int rounds = sh >= 1 ? 1 : (groups + grid - 1) / grid;
-        const int c = rounds * n * ((experts + max(sh, 1) - 1) / max(sh, 1));
-        if (c < cost || (c == cost && max(sh, 1) < shares)) {
+        const int sh = max(min(min(grid / groups, experts), FEW_MAX_SPLIT), 1);
+        const int rounds = (groups * sh + grid - 1) / grid;
+        const int c = rounds * n * ((experts + sh - 1) / sh);
+        if (c <= cost) {
             cost = c;
             best = n;
-            shares = max(sh, 1);
+            shares = sh;
         }
     }
     w.per = best;
@@ -264,43 +342,112 @@ __device__ __forceinline__ Pass next_pass(Work &w)
         p.tile = (int)(w.q - (int64_t)p.a * w.per);
         const int left = (int)min((int64_t)(w.per - p.tile), w.end - w.q);
         // equal passes
-        p.tiles = (left + (left + FEW_WARPS - 1) / FEW_WARPS - 1) /
-                  ((left + FEW_WARPS - 1) / FEW_WARPS);
+        p.tiles = (left + (left + FEW_TILES - 1) / FEW_TILES - 1) /
+                  ((left + FEW_TILES - 1) / FEW_TILES);
         w.q += p.tiles;
     }
     return p;
 }
 
-// W: the weights' type.  NG: groups of eight tokens that an expert may have.
+// EACH inputs of row `row` of x (UP) or h (DOWN) from input k on; zeros behind the end.
+template <bool DOWN, int EACH>
+__device__ __forceinline__ void few_load(float (&v)[EACH], const FewArgs &g, int row, int k, int K)
+{
+    if (k >= K) {  // K is a multiple of 8, and so of EACH
+#pragma unroll
+        for (int i = 0; i < EACH; i++)
+            v[i] = 0.0f;
+        return;
+    }
+    if constexpr (DOWN) {
+        const float4 *from = reinterpret_cast<const float4 *>(g.h + (int64_t)row * K + k);
+#pragma unroll
+        for (int i = 0; i < EACH / 4; i++) {
+            const float4 u = __ldcg(from + i);
+            v[4 * i] = u.x;
+            v[4 * i + 1] = u.y;
+            v[4 * i + 2] = u.z;
+            v[4 * i + 3] = u.w;
+        }
+    } else {
+        const uint2 *from = reinterpret_cast<const uint2 *>(g.x + (int64_t)row * K + k);
+#pragma unroll
+        for (int i = 0; i < EACH / 4; i++) {
+            const uint2 u = from[i];
+            v[4 * i] = bf16lo(u.x);
+            v[4 * i + 1] = bf16hi(u.x);
+            v[4 * i + 2] = bf16lo(u.y);
+            v[4 * i + 3] = bf16hi(u.y);
+        }
+    }
+}
+
+// Puts them into a row of a stage as the mma's lanes want them: of each 16 inputs,
+// lane c (of four) finds its four side by side, DOWN the second terms' behind them.
+// E4M3 weights (fp16): inputs 4c .. 4c + 3, as the codes lie in a word; bf16 weights:
+// 2c, 2c + 1, 2c + 8 and 2c + 9, as ldmatrix deals them.
+template <typename Act, bool DOWN, int EACH>
+__device__ __forceinline__ void few_store(uint32_t row, int in_block, const float (&v)[EACH])
+{
+    constexpr int SIZE = DOWN ? 4 : 2;  // bytes of an input
+    uint32_t first[EACH / 2], second[EACH / 2];
+#pragma unroll
+    for (int i = 0; i < EACH / 2; i++) {
+        first[i] = pair_bits(Act(), v[2 * i], v[2 * i + 1]);
+        if (DOWN) {
+            const float2 f = pair_values(Act(), first[i]);
+            second[i] = pair_bits(Act(), rest_of(v[2 * i], f.x), rest_of(v[2 * i + 1], f.y));
+        }
+    }
+    if constexpr (sizeof(Act) == 2 && EACH == 8) {
+        const uint32_t to = row + in_block * SIZE;
+        if (DOWN) {
+            sts128(to, make_uint4(first[0], first[1], second[0], second[1]));
+            sts128(to + 16, make_uint4(first[2], first[3], second[2], second[3]));
+        } else {
+            sts128(to, make_uint4(first[0], first[1], first[2], first[3]));
+        }
+    } else {
+        const int c = (in_block & 7) >> 1;  // the lane of the first pair; the next has the other
+        const uint32_t to =
+            row + ((in_block & ~15) + 4 * c) * SIZE + (in_block & 8 ? 4 : 0);
+#pragma unroll
+        for (int i = 0; i < EACH / 2; i++) {
+            sts32(to + i * 4 * SIZE, first[i]);
+            if (DOWN)
+                sts32(to + i * 4 * SIZE + 8, second[i]);
+        }
+    }
+}
+
+// W: the weights' type.  NG: groups of eight tokens that an entry may have.
 template <typename W, int NG, bool DOWN>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
     few_kernel(const __grid_constant__ FewMaps maps, const FewArgs g)
 {
     using TY = FewType<W>;
     constexpr bool FP8 = sizeof(W) == 1;
-    constexpr int TERMS = DOWN ? 2 : 1;
-    // a tile's rows 0-7, and from them to rows 8-15
-    constexpr int TILE_STEP = DOWN ? 2048 : 1024, HALF_STEP = DOWN ? 1024 : FEW_WARPS * 1024;
+    constexpr int CHAINS = DOWN ? 4 : 2;  // sums that do not wait for each other
+    using Act = typename TY::Act;
+    // bytes of a row of activations in a block, padded so that the rows of a group
+    // start in different banks: 4 inputs of both terms are 16 bytes, of one term 8
+    constexpr int PITCH = DOWN ? TY::KB * 4 + 64 : TY::KB * 2 + 32;
+    constexpr int GIVEN = 128 * NG;                  // sums of a tile
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                 ~(uintptr_t)1023);
     uint8_t *top = raw + FEW_SMEM;
     FewShared &sh = *reinterpret_cast<FewShared *>(top - sizeof(FewShared));
-    // DOWN: sums of 16 outputs x T tokens for each warp
-    float *sums = reinterpret_cast<float *>(top - sizeof(FewShared)) - FEW_WARPS * 16 * g.T;
+    // UP: for each tile the second slice's sums, on their way to the first; DOWN: for
+    // each warp the sums of 16 outputs x T tokens
+    float *sums = reinterpret_cast<float *>(top - sizeof(FewShared)) -
+                  (DOWN ? FEW_WARPS * 16 * g.T : FEW_TILES * GIVEN);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int K = DOWN ? g.I : g.H;
     const int blocks = (K + TY::KB - 1) / TY::KB;
 
     wait_prior_grid();
     allow_next_grid();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < FEW_MAX_STAGES; i++) {
-            mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), FEW_WARPS);
-        }
-        mbar_fence_init();
-    }
     if (!DOWN) {  // the second kernel's counters
         const int i = blockIdx.x * FEW_THREADS + threadIdx.x;
         if (i < g.groups)
@@ -308,30 +455,48 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
     few_lists(sh, g, !DOWN, !DOWN && blockIdx.x == 0 ? g.err_word : nullptr);
 
-    // rows of a stage's activations: all tokens of x, or the most that an expert has
-    const int act_rows = DOWN ? 16 << box_of(sh.longest) : (g.T + 7) & ~7;
+    // Stage: two blocks of inputs of up to `per` tiles, and of the activations of as
+    // many tokens as the largest entry has, in groups of eight.  Warp: tile
+    // warp % per, of slice warp / per; a pair of slices, a team, takes the two blocks
+    // of every stage in its own slots of the ring.  (Who waits on a slot's barriers
+    // does so in each of its phases: parity cannot tell a phase from the next but one.)
     const Work whole = few_work<DOWN>(sh, g);
-    const uint8_t *ring_end = DOWN ? reinterpret_cast<uint8_t *>(sums)
-                                   : top - sizeof(FewShared);
-    const int ring_bytes = (int)(ring_end - ring);
-    // DOWN: a CTA of few tiles splits the inputs over its warps as well, `slices`
-    // blocks a stage (as long as four stages fit); the slices' sums meet at the end
-    const int slice_w = DOWN ? whole.per * FEW_TILE : FEW_W_BYTES;
-    const int slice_bytes = slice_w + TY::WIDTH * act_rows * 128;
-    const int slices =
-        DOWN ? max(min(FEW_WARPS / whole.per, ring_bytes / (4 * slice_bytes)), 1) : 1;
-    const int stage_bytes = slices * slice_bytes;
-    // at least three: a slice is 48 KB at most, and the ring has 170
-    const int stages = min(ring_bytes / stage_bytes, FEW_MAX_STAGES);
+    const int per = DOWN ? whole.per : FEW_TILES;
+    int teams = FEW_WARPS / per / 2;  // pairs of slices
+    const int act_block = ((sh.longest + 7) & ~7) * PITCH;
+    const int w_bytes = 2 * per * FEW_TILE;
+    const int act_at = w_bytes + (FP8 ? FEW_FACTORS : 0);
+    const int stage_bytes = (act_at + 2 * act_block + 1023) & ~1023;
+    // at least two: a stage is 70 KB at most, and the ring has 140
+    int stages = min((int)(reinterpret_cast<uint8_t *>(sums) - ring) / stage_bytes,
+                     FEW_MAX_STAGES);
+    teams = min(teams, stages);
+    stages -= stages % teams;
+    const int slices = 2 * teams;
+    const bool pairs = K % TY::KB == 0;  // how the maps are made
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; i++) {
+            mbar_init(smem_addr(&sh.full[i]), 1);
+            mbar_init(smem_addr(&sh.ready[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), 2 * per);
+        }
+        for (int i = 0; i < FEW_TILES; i++) {
+            mbar_init(smem_addr(&sh.given[i]), 1);
+            mbar_init(smem_addr(&sh.taken[i]), 1);
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
+
     const int row_tiles = (g.H + 15) / 16;
     const int groups = DOWN ? (row_tiles + whole.per - 1) / whole.per : 0;
-    const int rounds = DOWN ? groups * whole.shares : (int)gridDim.x;
-    int s = 0;
-    uint32_t phase = 0;
-    int64_t issued = 0;
-    bool ok = true;  // false once one of this warp's waits gave up
+    const int jobs = DOWN ? groups * whole.shares : (int)gridDim.x;
+    int s = 0, turn = 0;  // the slot, and the team whose it is
+    uint32_t phase = 0, meetings = 0;
+    int64_t issued = 0;   // stages, of the producer
+    bool ok = true;       // false once one of this warp's waits gave up
 
-    for (int job = blockIdx.x; ok && job < rounds; job += gridDim.x) {
+    for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
         Work work = whole;
         if (DOWN) {
             const int group = job / whole.shares;
@@ -341,45 +506,95 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             work.q = (int64_t)sh.active * work.split / whole.shares;
             work.end = (int64_t)sh.active * (work.split + 1) / whole.shares;
         }
-        if (warp == FEW_WARPS) {
+
+        if (warp == FEW_WARPS) {  // producer
             while (ok && work.q < work.end) {
                 const Pass p = next_pass<DOWN>(work);
-                const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
-                const int box = box_of(n);
-                const int rows = DOWN ? 16 << box : g.T;  // of the activations' box
-                const int row = DOWN ? 2 * row0 : 0;
-                const CUtensorMap *act = &maps.act[DOWN ? box : 0];
+                const int e = sh.act[p.a];
                 const int wrow = p.tile * (DOWN ? 16 : 8);
-                for (int b0 = 0; b0 < blocks; b0 += slices) {
+                for (int b = 0; b < blocks; b += 2) {
                     if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
                     const uint32_t bar = smem_addr(&sh.full[s]);
-                    uint32_t at = smem_addr(ring) + s * stage_bytes;
-                    const int end = min(b0 + slices, blocks);
+                    const uint32_t at = smem_addr(ring) + s * stage_bytes;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(
-                            bar, (end - b0) * (p.tiles * FEW_TILE + TY::WIDTH * rows * 128));
-                        for (int b = b0; b < end; b++, at += slice_bytes) {
-                            int done = 0;  // tiles, in boxes of falling size
+                        mbar_arrive_expect_tx(bar, 2 * p.tiles * FEW_TILE);
+                        int done = 0;  // tiles, in boxes of falling size
 #pragma unroll
-                            for (int i = 3; i >= 0; i--) {
-                                if (!(p.tiles >> i & 1))
-                                    continue;
-                                const int r = wrow + done * (DOWN ? 16 : 8);
-                                tensor_g2s(at + done * TILE_STEP, &maps.w[i], b * TY::KB, r, e,
-                                           bar);
-                                if (!DOWN)
-                                    tensor_g2s(at + HALF_STEP + done * TILE_STEP, &maps.w[i],
-                                               b * TY::KB, g.I + r, e, bar);
-                                done += 1 << i;
+                        for (int i = 3; i >= 0; i--) {
+                            if (!(p.tiles >> i & 1))
+                                continue;
+                            const int r = wrow + done * (DOWN ? 16 : 8);
+                            const uint32_t to = at + done * 2 * FEW_TILE;
+                            if (pairs) {
+                                tensor5_g2s(to, &maps.w[i], 0, r, 0, b, e, bar);
+                            } else {
+                                tensor5_g2s(to, &maps.w[i], b * TY::KB, r, 0, 0, e, bar);
+                                tensor5_g2s(to + (FEW_TILE << i), &maps.w[i], (b + 1) * TY::KB, r,
+                                            0, 0, e, bar);
                             }
-#pragma unroll
-                            for (int i = 0; i < TY::WIDTH; i++)
-                                tensor_g2s(at + slice_w + i * act_rows * 128, act,
-                                           b * TY::KB + i * 64, row, 0, bar);
+                            done += 1 << i;
                         }
                     }
                     issued++;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            continue;
+        }
+
+        if (warp > FEW_WARPS) {  // feeders, each with slots of its own
+            constexpr int EACH = 2 * TY::KB / 32;  // inputs a lane brings of each token
+            constexpr int BATCH = 4;               // tokens in flight
+            const int block = lane >> 4, in_block = (lane & 15) * EACH;
+            while (ok && work.q < work.end) {
+                const Pass p = next_pass<DOWN>(work);
+                const int row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
+                for (int b = 0; b < blocks; b += 2) {
+                    if (s % FEW_FEEDERS == warp - FEW_WARPS - 1) {
+                        if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
+                            break;
+                        uint8_t *stage = ring + s * stage_bytes;
+                        float *factors = reinterpret_cast<float *>(stage + w_bytes);
+                        const uint32_t act = smem_addr(stage) + act_at + block * act_block;
+                        const int k = (b + block) * TY::KB + in_block;
+                        for (int j0 = 0; j0 < n; j0 += BATCH) {
+                            float v[BATCH][EACH];
+#pragma unroll
+                            for (int j = 0; j < BATCH; j++) {
+                                const int row = row0 + min(j0 + j, n - 1);
+                                few_load<DOWN, EACH>(v[j], g, DOWN ? row : sh.token[row], k, K);
+                            }
+#pragma unroll
+                            for (int j = 0; j < BATCH; j++) {
+                                if (j0 + j >= n)
+                                    break;
+                                if (FP8) {
+                                    uint32_t big = 0;  // as bits, so that NaN is the largest
+#pragma unroll
+                                    for (int i = 0; i < EACH; i++)
+                                        big = max(big, __float_as_uint(v[j][i]) & 0x7fffffffu);
+#pragma unroll
+                                    for (int d = 8; d > 0; d >>= 1)
+                                        big = max(big, __shfl_xor_sync(FULL_MASK, big, d));
+                                    float inverse;
+                                    const float f = to_half_range(big, inverse);
+                                    if ((lane & 15) == 0)
+                                        factors[block * FEW_ROWS + j0 + j] = inverse;
+#pragma unroll
+                                    for (int i = 0; i < EACH; i++)
+                                        v[j][i] *= f;
+                                }
+                                few_store<Act, DOWN, EACH>(act + (j0 + j) * PITCH, in_block, v[j]);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&sh.ready[s]));
+                    }
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1;
@@ -396,13 +611,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             __syncwarp();
         }
         const int r8 = lane >> 2, c4 = lane & 3;  // this lane's row (and row + 8) and columns
+        const int slice = warp / per, in_pass = warp - slice * per;
+        const bool member = slice < slices;
         while (ok && work.q < work.end) {
             const Pass p = next_pass<DOWN>(work);
             const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
-            const int slice = DOWN ? warp / whole.per : 0;
-            const int in_pass = DOWN ? warp - slice * whole.per : warp;
-            const bool busy = slice < slices && in_pass < p.tiles;
+            const bool busy = member && in_pass < p.tiles;
             const int tile = p.tile + in_pass;
+            // where the tile lies in a block, and how far a block's next tile's rows,
+            // its own rows 8-15 and the second block are
+            int box = 3, before = 0;
+            while (box > 0 && !(p.tiles >> box & 1 && in_pass < before + (1 << box))) {
+                before += p.tiles & 1 << box;
+                box--;
+            }
+            const int half_step = DOWN ? 1024 : 1024 << box;
+            const uint32_t tile_at = before * 2 * FEW_TILE + (slice & 1) * (FEW_TILE << box) +
+                                     (in_pass - before) * (DOWN ? 2048 : 1024) +
+                                     ((lane >> 3) & 1) * half_step + (lane & 7) * 128;
+            const uint32_t act_offset = act_at + (slice & 1) * act_block + r8 * PITCH + c4 * (DOWN ? 16 : 8);
             const float *s_lo = nullptr, *s_hi = nullptr;  // of rows 0-7 and 8-15
             float v_lo = 0.0f, v_hi = 0.0f;
             if (FP8 && busy) {
@@ -416,41 +643,37 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             }
             float acc[NG][4];
 #pragma unroll
-            for (int i = 0; i < NG; i++)
-                acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-            // where in a stage the activations of this lane's column begin (E4M3
-            // weights: column r8; bf16: row lane % 8 of ldmatrix)
-            uint32_t col_row[NG];
-#pragma unroll
             for (int i = 0; i < NG; i++) {
-                const int col = i * 8 + (FP8 ? r8 : lane & 7);
-                col_row[i] = DOWN ? 2 * col : col < n ? sh.token[row0 + col] : 0;
+                acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
             }
-            uint32_t nan_lo = 0, nan_hi = 0;
-            for (int b0 = 0, mine = 0; b0 < blocks; b0 += slices, mine++) {
-                const int b = b0 + slice;
-                if (FP8 && busy && (mine & 31) == 0) {  // of the next 32 blocks, one a lane
-                    const int at = min(b + lane * slices, blocks - 1);
-                    v_lo = s_lo[at];
-                    v_hi = s_hi[at];
+            for (int b0 = 0, mine = 0; b0 < blocks; b0 += 2) {
+                const bool take = member && turn == slice >> 1;
+                if (++turn == teams)
+                    turn = 0;
+                const int b = b0 + (slice & 1);
+                if (take) {
+                    if (FP8 && busy && (mine & 31) == 0) {  // of the next 32 blocks, one a lane
+                        const int at = min(b + lane * slices, blocks - 1);
+                        v_lo = s_lo[at];
+                        v_hi = s_hi[at];
+                    }
+                    if (!(ok = warp_wait2(smem_addr(&sh.ready[s]), phase, smem_addr(&sh.full[s]),
+                                          phase)))
+                        break;
                 }
-                if (!(ok = warp_wait(smem_addr(&sh.full[s]), phase)))
-                    break;
-                if (busy && b < blocks) {
-                    const uint32_t at =
-                        smem_addr(ring) + s * stage_bytes + slice * slice_bytes;
-                    const uint32_t wt = at + in_pass * TILE_STEP + ((lane >> 3) & 1) * HALF_STEP +
-                                        (lane & 7) * 128;
+                if (take && busy && b < blocks) {
+                    const uint8_t *stage = ring + s * stage_bytes;
+                    const uint32_t wt = smem_addr(stage) + tile_at;
                     uint32_t a[TY::STEPS][4];
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         uint32_t v[4];  // rows 0-7 and 8-15 of 16-byte pieces 2j and 2j + 1
                         ldsm4(wt + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4), v);
                         if constexpr (FP8) {
-                            widen(v[0], a[2 * j][0], a[2 * j][2], nan_lo);
-                            widen(v[1], a[2 * j][1], a[2 * j][3], nan_hi);
-                            widen(v[2], a[2 * j + 1][0], a[2 * j + 1][2], nan_lo);
-                            widen(v[3], a[2 * j + 1][1], a[2 * j + 1][3], nan_hi);
+                            widen(v[0], a[2 * j][0], a[2 * j][2]);
+                            widen(v[1], a[2 * j][1], a[2 * j][3]);
+                            widen(v[2], a[2 * j + 1][0], a[2 * j + 1][2]);
+                            widen(v[3], a[2 * j + 1][1], a[2 * j + 1][3]);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; i++)
@@ -462,47 +685,46 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                         f_lo = __shfl_sync(FULL_MASK, v_lo, mine & 31);
                         f_hi = __shfl_sync(FULL_MASK, v_hi, mine & 31);
                     }
+                    mine++;
+                    const uint32_t act = smem_addr(stage) + act_offset;
 #pragma unroll
                     for (int grp = 0; grp < NG; grp++) {
                         if (grp * 8 < n) {
-                            float part[2 * TERMS][4] = {};  // sums that do not wait for each other
+                            float part[CHAINS][4] = {};
+                            const uint32_t row = act + grp * 8 * PITCH;
 #pragma unroll
-                            for (int term = 0; term < TERMS; term++) {
-                                const uint32_t r = col_row[grp] + term;
-                                const uint32_t row = at + slice_w + r * 128;
-                                if constexpr (FP8) {
-                                    const uint32_t in = (c4 & 1) * 8;
-#pragma unroll
-                                    for (int j = 0; j < TY::STEPS; j++) {
-                                        const uint2 v = lds64(
-                                            row + (j >> 2) * act_rows * 128 + in +
-                                            ((((j & 3) * 2 + (c4 >> 1)) ^ (r & 7)) << 4));
-                                        mma16816(part[2 * term + (j & 1)], a[j], __byte_perm(v.x, v.y, 0x5410),
-                                                 __byte_perm(v.x, v.y, 0x7632));
-                                    }
+                            for (int j = 0; j < TY::STEPS; j++) {
+                                if (DOWN) {
+                                    const uint4 v = lds128(row + j * 64);
+                                    mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
+                                    mma_16816(Act(), part[2 + (j & 1) & CHAINS - 1], a[j], v.z, v.w);
                                 } else {
-#pragma unroll
-                                    for (int j = 0; j < TY::STEPS; j += 2) {
-                                        uint32_t v[4];
-                                        ldsm4(row + (((j * 2 + (lane >> 3)) ^ (r & 7)) << 4), v);
-                                        mma16816(part[2 * term], a[j], v[0], v[1]);
-                                        mma16816(part[2 * term + 1], a[j + 1], v[2], v[3]);
-                                    }
+                                    const uint2 v = lds64(row + j * 32);
+                                    mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
                                 }
                             }
+                            float2 back = make_float2(1.0f, 1.0f);  // the columns' powers of two
+                            if (FP8)
+                                back = *reinterpret_cast<const float2 *>(
+                                    stage + w_bytes +
+                                    ((slice & 1) * FEW_ROWS + grp * 8 + c4 * 2) * 4);
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
                                 float v = part[0][i] + part[1][i];
                                 if (DOWN)
-                                    v += part[2 * TERMS - 2][i] + part[2 * TERMS - 1][i];
-                                acc[grp][i] = fmaf(v, i < 2 ? f_lo : f_hi, acc[grp][i]);
+                                    v += part[CHAINS - 2][i] + part[CHAINS - 1][i];
+                                acc[grp][i] = fmaf(
+                                    v, (i < 2 ? f_lo : f_hi) * (i & 1 ? back.y : back.x),
+                                    acc[grp][i]);
                             }
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.empty[s]));
+                if (take) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.empty[s]));
+                }
                 if (++s == stages) {
                     s = 0;
                     phase ^= 1;
@@ -512,19 +734,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 break;
             if (!busy)
                 continue;
-            if (FP8) {  // a NaN code of a row makes the row NaN
-                nan_lo |= __shfl_xor_sync(FULL_MASK, nan_lo, 1);
-                nan_lo |= __shfl_xor_sync(FULL_MASK, nan_lo, 2);
-                nan_hi |= __shfl_xor_sync(FULL_MASK, nan_hi, 1);
-                nan_hi |= __shfl_xor_sync(FULL_MASK, nan_hi, 2);
-                const float bad = __int_as_float(0x7fffffff);
+            if (!DOWN) {  // the two slices' sums meet
+                float *x = sums + in_pass * GIVEN + lane;
+                const uint32_t now = meetings++ & 1;
+                if (slice == 1) {
+                    if (!(ok = warp_wait(smem_addr(&sh.taken[in_pass]), now ^ 1)))
+                        break;
 #pragma unroll
-                for (int i = 0; i < NG; i++) {
-                    if (nan_lo & 0x80808080u)
-                        acc[i][0] = acc[i][1] = bad;
-                    if (nan_hi & 0x80808080u)
-                        acc[i][2] = acc[i][3] = bad;
+                    for (int i = 0; i < 4 * NG; i++)
+                        x[i * 32] = acc[i / 4][i % 4];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.given[in_pass]));
+                    continue;
                 }
+                if (!(ok = warp_wait(smem_addr(&sh.given[in_pass]), now)))
+                    break;
+#pragma unroll
+                for (int i = 0; i < 4 * NG; i++)
+                    acc[i / 4][i % 4] += x[i * 32];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.taken[in_pass]));
             }
 #pragma unroll
             for (int grp = 0; grp < NG; grp++) {
@@ -537,20 +768,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                         float *to = sums + (warp * g.T + sh.token[row0 + col]) * 16 + r8;
                         to[0] += acc[grp][i];
                         to[8] += acc[grp][2 + i];
-                    } else {
-                        const float gate = acc[grp][i];
-                        const float v = gate / (1.0f + expf(-gate)) * acc[grp][2 + i] *
-                                        sh.w[row0 + col];
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                        const float rest = v - __bfloat162float(hi);  // NaN of an infinite v
-                        const __nv_bfloat16 lo =
-                            __float2bfloat16_rn(fabsf(rest) < 3.0e38f ? rest : 0.0f);
-                        __nv_bfloat16 *to = g.h + (int64_t)(row0 + col) * 2 * g.I + tile * 8 + r8;
-                        to[0] = hi;
-                        to[g.I] = lo;
+                        continue;
                     }
+                    const float gate = acc[grp][i];
+                    const float v =
+                        gate / (1.0f + expf(-gate)) * acc[grp][2 + i] * sh.w[row0 + col];
+                    g.h[(int64_t)(row0 + col) * g.I + tile * 8 + r8] = v;
                 }
             }
+            __syncwarp();
         }
 
         if (DOWN) {
@@ -568,7 +794,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             if (mine)
                 for (int t = lane >> 4; t < g.T; t += 2)
                     for (int i = 1; i < slices; i++)
-                        tile_sums[t * 16] += tile_sums[(i * whole.per * g.T + t) * 16];
+                        tile_sums[t * 16] += tile_sums[(i * per * g.T + t) * 16];
             if (whole.shares > 1) {
                 const int64_t plane = (int64_t)g.T * g.H;
                 if (mine)
@@ -621,6 +847,22 @@ cudaError_t few(const FewMaps &maps, const FewArgs &g, cudaStream_t stream)
     return launch_pdl(kernel, dim3(sm_count()), dim3(FEW_THREADS), FEW_SMEM, stream, maps, g);
 }
 
+// A map of weights [planes][halves][rows][cols] in boxes of two blocks of 128 bytes x
+// box_rows x halves, or of one block where rows are not whole blocks.
+cudaError_t few_map(CUtensorMap *map, CUtensorMapDataType type, int element, const void *base,
+                    int64_t planes, int halves, int64_t rows, int64_t cols, int box_rows)
+{
+    const int width = 128 / element;
+    const bool whole = cols % width == 0;
+    const int64_t row = cols * element;
+    const MapDim dims[5] = {{whole ? width : cols, 0, width},
+                            {rows, row, box_rows},
+                            {halves, rows * row, halves},
+                            {whole ? cols / width : 1, whole ? 128 : row, whole ? 2 : 1},
+                            {planes, halves * rows * row, 1}};
+    return encode_map(map, type, base, dims);
+}
+
 template <typename W, bool DOWN>
 cudaError_t few_for(const FewArgs &g, const void *weights, cudaStream_t stream)
 {
@@ -629,32 +871,23 @@ cudaError_t few_for(const FewArgs &g, const void *weights, cudaStream_t stream)
     FewMaps maps;
     cudaError_t st = cudaSuccess;
     for (int i = 0; i < 4 && st == cudaSuccess; i++)
-        st = DOWN ? encode_map(&maps.w[i], type, sizeof(W), weights, g.E, g.H, g.I, 16 << i,
-                               FewType<W>::KB)
-                  : encode_map(&maps.w[i], type, sizeof(W), weights, g.E, 2 * (int64_t)g.I, g.H,
-                               8 << i, FewType<W>::KB);
-    for (int i = 0; i < (DOWN ? 4 : 1) && st == cudaSuccess; i++)
-        st = DOWN ? encode_map(&maps.act[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.h, 1,
-                               2 * (int64_t)g.T * g.k, g.I, 16 << i, 64)
-                  : encode_map(&maps.act[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.x, 1, g.T,
-                               g.H, g.T, 64);
+        st = DOWN ? few_map(&maps.w[i], type, sizeof(W), weights, g.E, 1, g.H, g.I, 16 << i)
+                  : few_map(&maps.w[i], type, sizeof(W), weights, g.E, 2, g.I, g.H, 8 << i);
     if (st != cudaSuccess)
         return st;
-    // registers for the groups of eight that an expert can have at most
+    // registers for the groups of eight that an entry can have at most
     if (g.T <= 8)
         return few<W, 1, DOWN>(maps, g, stream);
     if (g.T <= 16)
         return few<W, 2, DOWN>(maps, g, stream);
-    if (g.T <= 32)
-        return few<W, 4, DOWN>(maps, g, stream);
-    return few<W, 8, DOWN>(maps, g, stream);
+    return few<W, 4, DOWN>(maps, g, stream);
 }
 
 size_t counters(int H) { return ((size_t)(H + 15) / 16 * sizeof(uint32_t) + 255) & ~(size_t)255; }
 
 size_t inner_bytes(int T, int k, int I)
 {
-    return ((size_t)T * k * 2 * I * sizeof(__nv_bfloat16) + 255) & ~(size_t)255;
+    return ((size_t)T * k * I * sizeof(float) + 255) & ~(size_t)255;
 }
 
 template <typename W>
@@ -695,7 +928,7 @@ cudaError_t launch_layer_few(int T, int k, int H, int I, int E, const void *x, c
     g.topk_w = topk_w;
     g.arrived = reinterpret_cast<uint32_t *>(ws);
     g.groups = (H + 15) / 16;
-    g.h = reinterpret_cast<__nv_bfloat16 *>(ws + counters(H));
+    g.h = reinterpret_cast<float *>(ws + counters(H));
     g.parts = reinterpret_cast<float *>(ws + counters(H) + inner_bytes(T, k, I));
     g.out = out;
     g.out_f32 = out_f32;

@@ -21,6 +21,16 @@ __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap *map,
         : "memory");
 }
 
+__device__ __forceinline__ void tensor5_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int u, int v, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -13,4 +13,12 @@ namespace moe {
 cudaError_t encode_map(CUtensorMap *map, CUtensorMapDataType type, int element, const void *base,
                        int64_t planes, int64_t rows, int64_t cols, int box_rows, int box_cols);
 
+// The same for any five dimensions (extent, stride in bytes, box), the first dense.
+struct MapDim {
+    int64_t extent, stride;
+    int box;
+};
+cudaError_t encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base,
+                       const MapDim (&dims)[5]);
+
 }  // namespace moe
