@@ -5,10 +5,10 @@
 // w[t,e] the sum of token t's weights over the slots that name e.  With few rows
 // an expert the layer is a stream of weights: every chosen expert's are read
 // once, at the rate of the HBM, and what is computed on the way has to keep up
-// with it.  A producer warp keeps a ring of stages in flight, two 128-byte-wide
-// blocks of the inputs each, in as few tensor copies as can be (issuing one takes
-// the warp some 100 cycles).  Three feeder warps run ahead beside it and put the
-// matching pieces of the entry's tokens into the stage.  A consumer warp takes 16
+// with it.  Four loader warps, each with slots of its own, keep a ring of stages in
+// flight, two 128-byte-wide blocks of the inputs each: the weights in as few tensor
+// copies as can be (issuing one takes the warp some 100 cycles), and the matching
+// pieces of the entry's tokens, converted on the way.  A consumer warp takes 16
 // weight rows (one mma tile) of its slice of the blocks and multiplies them with all
 // of the tokens (mma.sync, tokens as columns in groups of eight; an expert of more
 // than 32 tokens counts as two entries).  A tcgen05.mma would take at least 64 rows a
@@ -42,8 +42,8 @@ namespace {
 
 constexpr int FEW_WARPS = 16;   // consumers
 constexpr int FEW_TILES = 8;    // most tiles of a stage
-constexpr int FEW_FEEDERS = 3;  // warps that bring the activations
-constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1 + FEW_FEEDERS);
+constexpr int FEW_LOADERS = 4;
+constexpr int FEW_THREADS = 32 * (FEW_WARPS + FEW_LOADERS);
 constexpr int FEW_MAX_STAGES = 16;
 constexpr int FEW_ROWS = 32;      // most tokens of an entry
 constexpr int FEW_TILE = 2048;     // 16 rows x 128 bytes
@@ -349,35 +349,33 @@ __device__ __forceinline__ Pass next_pass(Work &w)
     return p;
 }
 
-// EACH inputs of row `row` of x (UP) or h (DOWN) from input k on; zeros behind the end.
+// EACH inputs of row `row` of x (UP, bf16) or h (DOWN, fp32) from input k on, as they
+// lie; zeros behind the end.  (K is a multiple of 8, and so of EACH.)
 template <bool DOWN, int EACH>
-__device__ __forceinline__ void few_load(float (&v)[EACH], const FewArgs &g, int row, int k, int K)
+__device__ __forceinline__ void few_load(uint32_t (&v)[DOWN ? EACH : EACH / 2], const FewArgs &g,
+                                         int row, int k, int K)
 {
-    if (k >= K) {  // K is a multiple of 8, and so of EACH
+    constexpr int WORDS = DOWN ? EACH : EACH / 2;
+    const int64_t at = (int64_t)row * K + k;
+    const void *from = DOWN ? static_cast<const void *>(g.h + at)
+                            : static_cast<const void *>(g.x + at);
+    const bool in = k < K;
+    if constexpr (WORDS == 2) {
+        uint2 u = make_uint2(0, 0);
+        if (in)
+            u = __ldcg(static_cast<const uint2 *>(from));
+        v[0] = u.x;
+        v[1] = u.y;
+    } else {
 #pragma unroll
-        for (int i = 0; i < EACH; i++)
-            v[i] = 0.0f;
-        return;
-    }
-    if constexpr (DOWN) {
-        const float4 *from = reinterpret_cast<const float4 *>(g.h + (int64_t)row * K + k);
-#pragma unroll
-        for (int i = 0; i < EACH / 4; i++) {
-            const float4 u = __ldcg(from + i);
+        for (int i = 0; i < WORDS / 4; i++) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in)
+                u = __ldcg(static_cast<const uint4 *>(from) + i);
             v[4 * i] = u.x;
             v[4 * i + 1] = u.y;
             v[4 * i + 2] = u.z;
             v[4 * i + 3] = u.w;
-        }
-    } else {
-        const uint2 *from = reinterpret_cast<const uint2 *>(g.x + (int64_t)row * K + k);
-#pragma unroll
-        for (int i = 0; i < EACH / 4; i++) {
-            const uint2 u = from[i];
-            v[4 * i] = bf16lo(u.x);
-            v[4 * i + 1] = bf16hi(u.x);
-            v[4 * i + 2] = bf16lo(u.y);
-            v[4 * i + 3] = bf16hi(u.y);
         }
     }
 }
@@ -418,6 +416,23 @@ __device__ __forceinline__ void few_store(uint32_t row, int in_block, const floa
                 sts32(to + i * 4 * SIZE + 8, second[i]);
         }
     }
+}
+
+// The largest magnitude, as bits (so that NaN is the largest), that a half-warp's
+// lanes hold.
+template <bool DOWN, int WORDS>
+__device__ __forceinline__ uint32_t few_largest(const uint32_t (&v)[WORDS])
+{
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < WORDS; i++)  // bf16: two at a time, in 16 bits each
+        big = DOWN ? max(big, v[i] & 0x7fffffffu) : __vmaxu2(big, v[i] & 0x7fff7fffu);
+    if (!DOWN)
+        big = max(big << 16, big & 0xffff0000u);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+        big = max(big, __shfl_xor_sync(FULL_MASK, big, d));
+    return big;
 }
 
 // W: the weights' type.  NG: groups of eight tokens that an entry may have.
@@ -493,7 +508,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     const int jobs = DOWN ? groups * whole.shares : (int)gridDim.x;
     int s = 0, turn = 0;  // the slot, and the team whose it is
     uint32_t phase = 0, meetings = 0;
-    int64_t issued = 0;   // stages, of the producer
+    uint32_t used = 0, parity = 0;  // a loader's slots that it filled, and their last phase
     bool ok = true;       // false once one of this warp's waits gave up
 
     for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
@@ -507,88 +522,82 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             work.end = (int64_t)sh.active * (work.split + 1) / whole.shares;
         }
 
-        if (warp == FEW_WARPS) {  // producer
-            while (ok && work.q < work.end) {
-                const Pass p = next_pass<DOWN>(work);
-                const int e = sh.act[p.a];
-                const int wrow = p.tile * (DOWN ? 16 : 8);
-                for (int b = 0; b < blocks; b += 2) {
-                    if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
-                        break;
-                    const uint32_t bar = smem_addr(&sh.full[s]);
-                    const uint32_t at = smem_addr(ring) + s * stage_bytes;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, 2 * p.tiles * FEW_TILE);
-                        int done = 0;  // tiles, in boxes of falling size
-#pragma unroll
-                        for (int i = 3; i >= 0; i--) {
-                            if (!(p.tiles >> i & 1))
-                                continue;
-                            const int r = wrow + done * (DOWN ? 16 : 8);
-                            const uint32_t to = at + done * 2 * FEW_TILE;
-                            if (pairs) {
-                                tensor5_g2s(to, &maps.w[i], 0, r, 0, b, e, bar);
-                            } else {
-                                tensor5_g2s(to, &maps.w[i], b * TY::KB, r, 0, 0, e, bar);
-                                tensor5_g2s(to + (FEW_TILE << i), &maps.w[i], (b + 1) * TY::KB, r,
-                                            0, 0, e, bar);
-                            }
-                            done += 1 << i;
-                        }
-                    }
-                    issued++;
-                    if (++s == stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            continue;
-        }
-
-        if (warp > FEW_WARPS) {  // feeders, each with slots of its own
+        if (warp >= FEW_WARPS) {  // loaders
             constexpr int EACH = 2 * TY::KB / 32;  // inputs a lane brings of each token
+            constexpr int WORDS = DOWN ? EACH : EACH / 2;
             constexpr int BATCH = 4;               // tokens in flight
             const int block = lane >> 4, in_block = (lane & 15) * EACH;
             while (ok && work.q < work.end) {
                 const Pass p = next_pass<DOWN>(work);
-                const int row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
+                const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
+                const int wrow = p.tile * (DOWN ? 16 : 8);
                 for (int b = 0; b < blocks; b += 2) {
-                    if (s % FEW_FEEDERS == warp - FEW_WARPS - 1) {
-                        if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
-                            break;
-                        uint8_t *stage = ring + s * stage_bytes;
-                        float *factors = reinterpret_cast<float *>(stage + w_bytes);
-                        const uint32_t act = smem_addr(stage) + act_at + block * act_block;
+                    if (s % FEW_LOADERS == warp - FEW_WARPS) {
                         const int k = (b + block) * TY::KB + in_block;
-                        for (int j0 = 0; j0 < n; j0 += BATCH) {
-                            float v[BATCH][EACH];
+                        uint32_t raws[BATCH][WORDS];
+                        auto load = [&](int j0) {
 #pragma unroll
                             for (int j = 0; j < BATCH; j++) {
                                 const int row = row0 + min(j0 + j, n - 1);
-                                few_load<DOWN, EACH>(v[j], g, DOWN ? row : sh.token[row], k, K);
+                                few_load<DOWN, EACH>(raws[j], g, DOWN ? row : sh.token[row], k,
+                                                     K);
                             }
+                        };
+                        load(0);  // in flight during the wait
+                        if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
+                            break;
+                        const uint32_t bar = smem_addr(&sh.full[s]);
+                        uint8_t *stage = ring + s * stage_bytes;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(bar, 2 * p.tiles * FEW_TILE);
+                            int done = 0;  // tiles, in boxes of falling size
+#pragma unroll
+                            for (int i = 3; i >= 0; i--) {
+                                if (!(p.tiles >> i & 1))
+                                    continue;
+                                const int r = wrow + done * (DOWN ? 16 : 8);
+                                const uint32_t to = smem_addr(stage) + done * 2 * FEW_TILE;
+                                if (pairs) {
+                                    tensor5_g2s(to, &maps.w[i], 0, r, 0, b, e, bar);
+                                } else {
+                                    tensor5_g2s(to, &maps.w[i], b * TY::KB, r, 0, 0, e, bar);
+                                    tensor5_g2s(to + (FEW_TILE << i), &maps.w[i],
+                                                (b + 1) * TY::KB, r, 0, 0, e, bar);
+                                }
+                                done += 1 << i;
+                            }
+                        }
+                        __syncwarp();
+                        used |= 1u << s;
+                        parity = (parity & ~(1u << s)) | phase << s;
+                        float *factors =
+                            reinterpret_cast<float *>(stage + w_bytes) + block * FEW_ROWS;
+                        const uint32_t act = smem_addr(stage) + act_at + block * act_block;
+                        for (int j0 = 0; j0 < n; j0 += BATCH) {
+                            if (j0 > 0)
+                                load(j0);
 #pragma unroll
                             for (int j = 0; j < BATCH; j++) {
                                 if (j0 + j >= n)
                                     break;
+                                float f = 1.0f;
                                 if (FP8) {
-                                    uint32_t big = 0;  // as bits, so that NaN is the largest
-#pragma unroll
-                                    for (int i = 0; i < EACH; i++)
-                                        big = max(big, __float_as_uint(v[j][i]) & 0x7fffffffu);
-#pragma unroll
-                                    for (int d = 8; d > 0; d >>= 1)
-                                        big = max(big, __shfl_xor_sync(FULL_MASK, big, d));
                                     float inverse;
-                                    const float f = to_half_range(big, inverse);
+                                    f = to_half_range(few_largest<DOWN, WORDS>(raws[j]), inverse);
                                     if ((lane & 15) == 0)
-                                        factors[block * FEW_ROWS + j0 + j] = inverse;
-#pragma unroll
-                                    for (int i = 0; i < EACH; i++)
-                                        v[j][i] *= f;
+                                        factors[j0 + j] = inverse;
                                 }
-                                few_store<Act, DOWN, EACH>(act + (j0 + j) * PITCH, in_block, v[j]);
+                                float v[EACH];
+#pragma unroll
+                                for (int i = 0; i < WORDS; i++) {
+                                    if constexpr (DOWN) {
+                                        v[i] = __uint_as_float(raws[j][i]) * f;
+                                    } else {
+                                        v[2 * i] = bf16lo(raws[j][i]) * f;
+                                        v[2 * i + 1] = bf16hi(raws[j][i]) * f;
+                                    }
+                                }
+                                few_store<Act, DOWN, EACH>(act + (j0 + j) * PITCH, in_block, v);
                             }
                         }
                         __syncwarp();
@@ -829,9 +838,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 }
         }
     }
-    if (warp == FEW_WARPS)  // copies still in flight land before the CTA may end
-        for (int64_t i = issued > stages ? issued - stages : 0; i < issued; i++)
-            ok = warp_wait(smem_addr(&sh.full[i % stages]), (i / stages) & 1) && ok;
+    // copies still in flight land before the CTA may end
+    for (int i = 0; warp >= FEW_WARPS && i < stages; i++)
+        if (used >> i & 1)
+            ok = warp_wait(smem_addr(&sh.full[i]), parity >> i & 1) && ok;
     if (!ok)
         report(g.err_word, MOE_ERRBIT_TIMEOUT);
 }
