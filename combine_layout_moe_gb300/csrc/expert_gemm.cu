@@ -14,9 +14,10 @@
 // One persistent CTA per SM, 128 rows x 256 outputs a tile:
 //   warps 0-7   promotion: warp w holds rows 32 (w % 4) .. +31, a thread one
 //               row and 2 x 64 outputs; then the epilogue
-//   warp 8      (with 9 to 11 a warpgroup of few registers) tensor copies: a block of the rows (boxes of 32 rows, only
-//               those of the segment) and of the weights (2 x 128 outputs)
-//   warp 9      issues the MMAs
+//   warp 8      tensor copies, one of a block of the rows (a box of 128, 64 or 32) and
+//               one of the weights (2 x 128 outputs): issuing one takes some 100 cycles
+//   warps 9,10  issue the MMAs, blocks in turn, each into its half of tensor memory (a
+//               block's waits, MMAs and commits take a warp longer than the MMAs)
 // For SwiGLU the two 128-output halves are gate and up of the same 128
 // channels, which makes a row's quantisation block the tile's own.
 #include <cuda_bf16.h>
@@ -38,7 +39,6 @@ constexpr int G_THREADS = 384;  // three warpgroups
 constexpr int G_PROMOTE = 256;  // threads of the promotion warps
 constexpr int G_ROWS = 128;
 constexpr int G_COLS = 256;
-constexpr int G_BOX = 32;  // rows of one tensor copy of a
 constexpr int G_STAGES = 4;
 constexpr int G_A_BYTES = G_ROWS * 128;
 constexpr int G_B_HALF = 128 * 128;
@@ -55,8 +55,15 @@ struct GemmShared {
 
 constexpr size_t G_SMEM = 1024 + (size_t)G_STAGES * G_STAGE + sizeof(GemmShared);
 
+// Rows in boxes of 32, 64 and 128; weights in one box of both halves, or (`halves`)
+// in one for each.
+struct GemmMaps {
+    CUtensorMap a[3], w;
+};
+
 struct GemmArgs {
     int N, kb, M, E, col_tiles;  // kb: blocks of 128 inputs; M: outputs (SwiGLU: I)
+    bool halves;
     const float *a_s, *w_s;
     const int32_t *offsets;
     void *out;
@@ -83,8 +90,7 @@ __device__ __forceinline__ GemmTile gemm_tile(const Segments &s, const GemmArgs 
 
 template <int OUT, bool TRANS>
 __global__ void __launch_bounds__(G_THREADS, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_w, const GemmArgs g)
+    expert_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g)
 {
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
@@ -104,8 +110,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         for (int i = 0; i < 4; i++)
             mbar_init(smem_addr(&sh.amax_full[i]), 2);
         mbar_fence_init();
-        prefetch_map(&map_a);
-        prefetch_map(&map_w);
+        prefetch_map(&maps.a[2]);
+        prefetch_map(&maps.w);
     }
     if (warp == 9)
         tmem_alloc(smem_addr(&sh.tmem), 512);
@@ -118,36 +124,32 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     bool ok = true;  // false once one of this thread's waits gave up
 
     // the promotion warps hold 128 running sums each thread: the third
-    // warpgroup gives them its registers (168 at launch: 72 + 2 x 216 = 3 x 168)
+    // warpgroup gives warpgroup gives them its registers (168 at launch: 56 + 2 x 224 = 3 x 168)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8) {
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
             for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
                 const GemmTile t = gemm_tile(sh.seg, g, tile);
-                const int boxes = (t.rows + G_BOX - 1) / G_BOX;
+                const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
+                const uint32_t bytes = (32 << box) * 128 + 2 * G_B_HALF;
                 const int c0 = OUT == OUT_SWIGLU ? t.col * 128 : t.col * G_COLS;
-                const int c1 = OUT == OUT_SWIGLU ? g.M + c0 : c0 + 128;
                 for (int b = 0; b < g.kb; b++) {
                     if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
                     const uint32_t bar = smem_addr(&sh.full[s]);
-                    const uint32_t at = smem_addr(stages + s * G_STAGE);
+                    const uint32_t at = smem_addr(stages + s * G_STAGE), wt = at + G_A_BYTES;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, boxes * G_BOX * 128 + 2 * G_B_HALF);
-                        for (int i = 0; i < boxes; i++)
-                            tensor_g2s(at + i * G_BOX * 128, &map_a, b * 128, t.row + i * G_BOX,
-                                       0, bar);
-                        const uint32_t wt = at + G_A_BYTES;
-                        if (TRANS) {
-                            tensor_g2s(wt, &map_w, c0, b * 128, t.expert, bar);
-                            tensor_g2s(wt + G_B_HALF, &map_w, c1, b * 128, t.expert, bar);
-                        } else {
-                            tensor_g2s(wt, &map_w, b * 128, c0, t.expert, bar);
-                            tensor_g2s(wt + G_B_HALF, &map_w, b * 128, c1, t.expert, bar);
-                        }
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tensor5_g2s(wt, &maps.w, TRANS && g.halves ? c0 : TRANS ? 0 : b * 128,
+                                    TRANS ? b * 128 : c0, TRANS && !g.halves ? 2 * t.col : 0, 0,
+                                    t.expert, bar);
+                        if (TRANS && g.halves)
+                            tensor5_g2s(wt + G_B_HALF, &maps.w, c0 + 128, b * 128, 0, 0, t.expert,
+                                        bar);
+                        tensor_g2s(at, &maps.a[box], b * 128, t.row, 0, bar);
                     }
                     issued++;
                     if (++s == G_STAGES) {
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             // copies still in flight land before the CTA may end
             for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
                 ok = warp_wait(smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
-        } else if (warp == 9) {
+        } else if (warp <= 10) {
+            const uint32_t own = warp - 9;  // half of tensor memory, and parity of its stages
             constexpr uint32_t idesc = mma_desc(G_ROWS, G_COLS, 0, false, TRANS);
             const uint32_t base = smem_addr(stages);
             // rows of 128 inputs: the next 32 are 32 bytes on.  Outputs contiguous:
@@ -167,42 +170,44 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             constexpr uint32_t b_step = (TRANS ? 4096 : 32) >> 4, a_step = 32 >> 4;
             const uint64_t a0 = smem_desc(base, 16, 1024);
             const uint64_t b0 = smem_desc(base + G_A_BYTES, TRANS ? G_B_HALF : 16, 1024);
-            int s = 0, d = 0;
-            uint32_t phase = 0, d_phase = 0;
-            int64_t issued = 0;
+            int s = 0;
+            uint32_t phase = 0, d_phase = 0, used = 0, parity = 0;
             for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
                 for (int b = 0; b < g.kb; b++) {
-                    if (!(ok = warp_wait2(smem_addr(&sh.sums_empty[d]), d_phase ^ 1,
-                                          smem_addr(&sh.full[s]), phase)))
-                        break;
-                    tcgen05_after_sync();
-                    const uint64_t da = a0 + (uint32_t)(s * (G_STAGE >> 4));
-                    const uint64_t db = b0 + (uint32_t)(s * (G_STAGE >> 4));
-                    const uint32_t to = tmem + d * G_COLS;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            mma_f8(to, da + i * a_step, db + i * b_step, idesc, i > 0);
-                        tcgen05_commit(smem_addr(&sh.sums_full[d]));
-                        tcgen05_commit(smem_addr(&sh.empty[s]));
-                    }
-                    issued++;
+                    const int at = s;
+                    const uint32_t at_phase = phase;
                     if (++s == G_STAGES) {
                         s = 0;
                         phase ^= 1;
                     }
-                    if (++d == 2) {
-                        d = 0;
-                        d_phase ^= 1;
+                    if ((at & 1) != own)
+                        continue;
+                    if (!(ok = warp_wait2(smem_addr(&sh.sums_empty[own]), d_phase ^ 1,
+                                          smem_addr(&sh.full[at]), at_phase)))
+                        break;
+                    tcgen05_after_sync();
+                    const uint64_t da = a0 + (uint32_t)(at * (G_STAGE >> 4));
+                    const uint64_t db = b0 + (uint32_t)(at * (G_STAGE >> 4));
+                    const uint32_t to = tmem + own * G_COLS;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            mma_f8(to, da + i * a_step, db + i * b_step, idesc, i > 0);
+                        tcgen05_commit(smem_addr(&sh.sums_full[own]));
+                        tcgen05_commit(smem_addr(&sh.empty[at]));
                     }
+                    d_phase ^= 1;
+                    used |= 1u << at;
+                    parity = (parity & ~(1u << at)) | at_phase << at;
                 }
             }
             // and so do the MMAs' arrivals
-            for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
-                ok = warp_wait(smem_addr(&sh.empty[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+            for (int i = 0; i < G_STAGES; i++)
+                if (used >> i & 1)
+                    ok = warp_wait(smem_addr(&sh.empty[i]), parity >> i & 1) && ok;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int half = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
@@ -282,17 +287,22 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     break;
                 if (busy) {
                     tcgen05_after_sync();
+                    // the next 32 sums are on their way while these are added
+                    const uint32_t from = mine + d * G_COLS;
+                    uint32_t p[2][32];
+                    tmem_ld32(from, p[0]);
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
-                        uint32_t p[32];
-                        tmem_ld32(mine + d * G_COLS + (q >> 1) * 128 + (q & 1) * 32, p);
                         tmem_wait_ld();
+                        if (q < 3)
+                            tmem_ld32(from + ((q + 1) >> 1) * 128 + ((q + 1) & 1) * 32,
+                                      p[(q + 1) & 1]);
                         const float f = q >> 1 ? f1 : f0;
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
                             float2 &c = acc[q >> 1][(q & 1) * 16 + i];
-                            c = fma2(make_float2(__uint_as_float(p[2 * i]),
-                                                 __uint_as_float(p[2 * i + 1])),
+                            c = fma2(make_float2(__uint_as_float(p[q & 1][2 * i]),
+                                                 __uint_as_float(p[q & 1][2 * i + 1])),
                                      make_float2(f, f), c);
                         }
                     }
@@ -404,18 +414,39 @@ cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uin
     if (st != cudaSuccess)
         return st;
     const int64_t wide = OUT == OUT_SWIGLU ? 2 * (int64_t)g.M : g.M;
-    CUtensorMap map_a, map_w;
-    st = encode_map(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a_q, 1, g.N, K, G_BOX, 128);
-    if (st != cudaSuccess)
-        return st;
-    st = encode_map(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q, g.E, TRANS ? K : wide,
-                    TRANS ? wide : K, 128, 128);
+    GemmMaps maps;
+    constexpr CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    for (int i = 0; i < 3; i++) {
+        st = encode_map(&maps.a[i], type, 1, a_q, 1, g.N, K, 32 << i, 128);
+        if (st != cudaSuccess)
+            return st;
+    }
+    GemmArgs args = g;
+    if (TRANS) {
+        // pieces of 128 outputs as a dimension of their own, where all are whole
+        args.halves = wide % 128 != 0;
+        const MapDim dims[5] = {{args.halves ? wide : 128, 0, 128},
+                                {K, wide, 128},
+                                {args.halves ? 1 : wide / 128, 128, args.halves ? 1 : 2},
+                                {1, wide * K, 1},
+                                {g.E, wide * K, 1}};
+        st = encode_map(&maps.w, type, w_q, dims);
+    } else {
+        // SwiGLU: gate and up; else 256 outputs
+        const int64_t rows = OUT == OUT_SWIGLU ? g.M : wide, parts = wide / rows;
+        const MapDim dims[5] = {{K, 0, 128},
+                                {rows, K, OUT == OUT_SWIGLU ? 128 : 256},
+                                {parts, rows * K, (int)parts},
+                                {1, wide * K, 1},
+                                {g.E, wide * K, 1}};
+        st = encode_map(&maps.w, type, w_q, dims);
+    }
     if (st != cudaSuccess)
         return st;
     // no more CTAs than tiles can be (each expert may add one partial row tile)
     const int64_t most = ((int64_t)g.N / G_ROWS + (g.E < g.N ? g.E : g.N)) * g.col_tiles;
     const int grid = (int)(most < sm_count() ? most : sm_count());
-    return launch_pdl(kernel, dim3(grid), dim3(G_THREADS), G_SMEM, stream, map_a, map_w, g);
+    return launch_pdl(kernel, dim3(grid), dim3(G_THREADS), G_SMEM, stream, maps, args);
 }
 
 }  // namespace
@@ -427,8 +458,8 @@ cudaError_t launch_expert_gemm(int N, int K, int M, int E, const uint8_t *a_q, c
 {
     if (N == 0)
         return cudaSuccess;
-    const GemmArgs g = {N,   K / 128, M, E, (M + G_COLS - 1) / G_COLS, a_s, w_s, offsets, out,
-                        nullptr, err_word};
+    const GemmArgs g = {N,   K / 128, M, E, (M + G_COLS - 1) / G_COLS, false, a_s, w_s, offsets,
+                        out, nullptr, err_word};
     if (transpose_w)
         return out_f32 ? run_gemm<OUT_F32, true>(g, K, a_q, w_q, stream)
                        : run_gemm<OUT_BF16, true>(g, K, a_q, w_q, stream);
@@ -442,7 +473,7 @@ cudaError_t launch_expert_swiglu(int N, int K, int I, int E, const uint8_t *a_q,
 {
     if (N == 0)
         return cudaSuccess;
-    const GemmArgs g = {N, K / 128, I, E, I / 128, a_s, w_s, offsets, h_q, h_s, err_word};
+    const GemmArgs g = {N, K / 128, I, E, I / 128, false, a_s, w_s, offsets, h_q, h_s, err_word};
     return run_gemm<OUT_SWIGLU, false>(g, K, a_q, w_q, stream);
 }
 
