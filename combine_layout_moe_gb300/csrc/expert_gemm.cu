@@ -43,6 +43,7 @@ constexpr int G_STAGES = 4;
 constexpr int G_A_BYTES = G_ROWS * 128;
 constexpr int G_B_HALF = 128 * 128;
 constexpr int G_STAGE = G_A_BYTES + 2 * G_B_HALF;
+constexpr int G_OUT = 32 * 64;  // a promotion warp's way out: 64 bytes of each of its rows
 
 struct GemmShared {
     uint64_t full[G_STAGES], empty[G_STAGES];
@@ -53,7 +54,9 @@ struct GemmShared {
     Segments seg;
 };
 
-constexpr size_t G_SMEM = 1024 + (size_t)G_STAGES * G_STAGE + sizeof(GemmShared);
+constexpr size_t G_SMEM =
+    1024 + (size_t)G_STAGES * G_STAGE + G_PROMOTE / 32 * G_OUT + sizeof(GemmShared);
+static_assert(G_SMEM <= 227 * 1024, "shared memory of one CTA");
 
 // Rows in boxes of 32, 64 and 128; weights in one box of both halves, or (`halves`)
 // in one for each.
@@ -71,37 +74,111 @@ struct GemmArgs {
     uint32_t *err_word;
 };
 
+// What one CTA does at a time.  `pair`: the cluster's other CTA does the next row tile
+// of the same columns.
 struct GemmTile {
     int expert, row, rows, col;
+    bool pair, store;
 };
 
-__device__ __forceinline__ GemmTile gemm_tile(const Segments &s, const GemmArgs &g, int tile)
+// Units of an expert of `rows` rows: tiles, or for clusters of two pairs of row tiles
+// times columns and, for an odd row tile, pairs of columns.
+template <int CLUSTER>
+__device__ __forceinline__ int gemm_units(int rows, int cols)
+{
+    const int tiles = (rows + G_ROWS - 1) / G_ROWS;
+    return CLUSTER == 1 ? tiles * cols : tiles / 2 * cols + (tiles & 1) * ((cols + 1) / 2);
+}
+
+// Row tiles vary fastest: neighbours in time share the expert's weights.
+template <int CLUSTER>
+__device__ __forceinline__ GemmTile gemm_tile(const Segments &s, const GemmArgs &g, int unit,
+                                              int rank)
 {
     GemmTile t;
-    t.expert = expert_of_tile(s, g.E, tile / g.col_tiles);
-    const int before = s.first[t.expert], tiles = s.first[t.expert + 1] - before;
-    const int local = tile - before * g.col_tiles;
-    // the expert's row tiles vary fastest: neighbours in time share its weights
-    t.row = s.lo[t.expert] + local % tiles * G_ROWS;
-    t.rows = min(G_ROWS, s.hi[t.expert] - t.row);
-    t.col = local / tiles;
+    t.expert = expert_of_unit(s, g.E, unit);
+    const int lo = s.lo[t.expert], hi = s.hi[t.expert];
+    const int tiles = (hi - lo + G_ROWS - 1) / G_ROWS;
+    int local = unit - s.first[t.expert], m;
+    t.pair = false;
+    t.store = true;
+    if (CLUSTER == 1) {
+        m = local % tiles;
+        t.col = local / tiles;
+    } else if (local < tiles / 2 * g.col_tiles) {
+        m = local % (tiles / 2) * 2 + rank;
+        t.col = local / (tiles / 2);
+        t.pair = true;
+    } else {
+        local -= tiles / 2 * g.col_tiles;
+        m = tiles - 1;
+        t.col = local * 2 + rank;
+        if (t.col >= g.col_tiles) {  // nothing left for this CTA: it keeps step
+            t.col = g.col_tiles - 1;
+            t.store = false;
+        }
+    }
+    t.row = lo + m * G_ROWS;
+    t.rows = min(G_ROWS, hi - t.row);
     return t;
 }
 
-template <int OUT, bool TRANS>
+// One half (128 outputs) of a tile's weights of block b into a stage, or the box of both.
+template <int OUT, bool TRANS, bool MULTICAST>
+__device__ __forceinline__ void weight_half(uint32_t wt, const CUtensorMap &map, const GemmArgs &g,
+                                            const GemmTile &t, int b, int half, uint32_t bar)
+{
+    const int o = OUT == OUT_SWIGLU ? t.col * 128 : t.col * G_COLS + half * 128;
+    const int x = TRANS ? (g.halves ? o : 0) : b * 128, y = TRANS ? b * 128 : o;
+    const int z = OUT == OUT_SWIGLU ? half : TRANS && !g.halves ? o / 128 : 0;
+    const uint32_t to = wt + half * G_B_HALF;
+    if (MULTICAST)
+        tensor5_g2s_multicast(to, &map, x, y, z, 0, t.expert, bar, 3);
+    else
+        tensor5_g2s(to, &map, x, y, z, 0, t.expert, bar);
+}
+
+// 64 bytes of each of a warp's rows, a row's with its lane, to global memory: rows side
+// by side in shared memory on the way, so that a store covers whole sectors.  `to` is
+// row 0's place; `bytes` are left of the row there, `rows` rows are there.
+__device__ __forceinline__ void store_rows(uint8_t *way, const uint32_t (&v)[16], uint8_t *to,
+                                           int64_t stride, int bytes, int rows)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        *reinterpret_cast<uint4 *>(way + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    __syncwarp();
+    const int piece = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 u =
+            *reinterpret_cast<const uint4 *>(way + r * 64 + (piece ^ (r >> 1 & 3)) * 16);
+        if (r < rows && piece * 16 < bytes)
+            st_v4(to + r * stride + piece * 16, u);
+    }
+}
+
+template <int OUT, bool TRANS, int CLUSTER>
 __global__ void __launch_bounds__(G_THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g)
 {
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    GemmShared &sh = *reinterpret_cast<GemmShared *>(stages + G_STAGES * G_STAGE);
+    uint8_t *ways = stages + G_STAGES * G_STAGE;
+    GemmShared &sh = *reinterpret_cast<GemmShared *>(ways + G_PROMOTE / 32 * G_OUT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CLUSTER > 1 ? (int)cluster_rank() : 0;
+    const int first_unit = blockIdx.x / CLUSTER, unit_step = gridDim.x / CLUSTER;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < G_STAGES; i++) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), CLUSTER);  // the MMAs of all CTAs
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&sh.sums_full[i]), 1);
@@ -116,26 +193,30 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     if (warp == 9)
         tmem_alloc(smem_addr(&sh.tmem), 512);
     wait_prior_grid();
-    load_segments(sh.seg, g.offsets, g.E, g.N, G_ROWS, blockIdx.x == 0 ? g.err_word : nullptr);
+    load_segments(
+        sh.seg, g.offsets, g.E, g.N,
+        [&](int rows) { return gemm_units<CLUSTER>(rows, g.col_tiles); },
+        blockIdx.x == 0 ? g.err_word : nullptr);
+    if (CLUSTER > 1)
+        cluster_sync();  // the other's barriers are ready too
     allow_next_grid();
     tcgen05_after_sync();
     const uint32_t tmem = sh.tmem;
-    const int tiles = sh.seg.first[g.E] * g.col_tiles;
+    const int units = sh.seg.first[g.E];
     bool ok = true;  // false once one of this thread's waits gave up
 
-    // the promotion warps hold 128 running sums each thread: the third
-    // warpgroup gives warpgroup gives them its registers (168 at launch: 56 + 2 x 224 = 3 x 168)
+    // the promotion warps hold 128 running sums a thread: the third warpgroup gives
+    // them its registers (168 at launch: 56 + 2 x 224 = 3 x 168)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8) {
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-                const GemmTile t = gemm_tile(sh.seg, g, tile);
+            for (int unit = first_unit; ok && unit < units; unit += unit_step) {
+                const GemmTile t = gemm_tile<CLUSTER>(sh.seg, g, unit, rank);
                 const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
                 const uint32_t bytes = (32 << box) * 128 + 2 * G_B_HALF;
-                const int c0 = OUT == OUT_SWIGLU ? t.col * 128 : t.col * G_COLS;
                 for (int b = 0; b < g.kb; b++) {
                     if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
@@ -143,12 +224,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     const uint32_t at = smem_addr(stages + s * G_STAGE), wt = at + G_A_BYTES;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(bar, bytes);
-                        tensor5_g2s(wt, &maps.w, TRANS && g.halves ? c0 : TRANS ? 0 : b * 128,
-                                    TRANS ? b * 128 : c0, TRANS && !g.halves ? 2 * t.col : 0, 0,
-                                    t.expert, bar);
-                        if (TRANS && g.halves)
-                            tensor5_g2s(wt + G_B_HALF, &maps.w, c0 + 128, b * 128, 0, 0, t.expert,
-                                        bar);
+                        if (CLUSTER > 1 && t.pair) {  // one half each, for both
+                            weight_half<OUT, TRANS, true>(wt, maps.w, g, t, b, rank, bar);
+                        } else if (CLUSTER > 1 || (TRANS && g.halves)) {
+                            weight_half<OUT, TRANS, false>(wt, maps.w, g, t, b, 0, bar);
+                            weight_half<OUT, TRANS, false>(wt, maps.w, g, t, b, 1, bar);
+                        } else {  // a box of both
+                            weight_half<OUT, TRANS, false>(wt, maps.w, g, t, b, 0, bar);
+                        }
                         tensor_g2s(at, &maps.a[box], b * 128, t.row, 0, bar);
                     }
                     issued++;
@@ -172,7 +255,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const uint64_t b0 = smem_desc(base + G_A_BYTES, TRANS ? G_B_HALF : 16, 1024);
             int s = 0;
             uint32_t phase = 0, d_phase = 0, used = 0, parity = 0;
-            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            for (int unit = first_unit; ok && unit < units; unit += unit_step) {
                 for (int b = 0; b < g.kb; b++) {
                     const int at = s;
                     const uint32_t at_phase = phase;
@@ -194,7 +277,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         for (int i = 0; i < 4; i++)
                             mma_f8(to, da + i * a_step, db + i * b_step, idesc, i > 0);
                         tcgen05_commit(smem_addr(&sh.sums_full[own]));
-                        tcgen05_commit(smem_addr(&sh.empty[at]));
+                        if (CLUSTER > 1)
+                            tcgen05_commit_multicast(smem_addr(&sh.empty[at]), 3);
+                        else
+                            tcgen05_commit(smem_addr(&sh.empty[at]));
                     }
                     d_phase ^= 1;
                     used |= 1u << at;
@@ -247,14 +333,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             load_rows(0);
             load_weights(0);
         };
+        uint8_t *way = ways + warp * G_OUT;
         int d = 0;
         uint32_t d_phase = 0, turn = 0;
         GemmTile next;
-        if (blockIdx.x < tiles) {
-            next = gemm_tile(sh.seg, g, blockIdx.x);
+        if (first_unit < units) {
+            next = gemm_tile<CLUSTER>(sh.seg, g, first_unit, rank);
             open_tile(next);
         }
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        for (int unit = first_unit; ok && unit < units; unit += unit_step) {
             const GemmTile t = next;
             const bool busy = quarter * 32 < t.rows;  // of the warp
             float2 acc[2][32];
@@ -262,67 +349,64 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             for (int i = 0; i < 32; i++)
                 acc[0][i] = acc[1][i] = make_float2(0.0f, 0.0f);
             float c_row[4], c_w0 = 0.0f, c_w1 = 0.0f;
-            for (int b = 0; b < g.kb; b++) {
-                if ((b & 31) == 0) {
+            for (int b0 = 0; ok && b0 < g.kb; b0 += 4) {
+                if ((b0 & 31) == 0) {
                     c_w0 = s_w0;
                     c_w1 = s_w1;
-                    if (b + 32 < g.kb)
-                        load_weights(b + 32);
+                    if (b0 + 32 < g.kb)
+                        load_weights(b0 + 32);
                 }
-                if ((b & 3) == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        c_row[i] = s_row[i];
-                    if (b + 4 < g.kb)
-                        load_rows(b + 4);
-                }
-                const float sr = c_row[0];
-                c_row[0] = c_row[1];
-                c_row[1] = c_row[2];
-                c_row[2] = c_row[3];
-                const float f0 = sr * __shfl_sync(FULL_MASK, c_w0, b & 31);
-                const float f1 = sr * __shfl_sync(FULL_MASK, c_w1, b & 31);
-                ok = warp_wait(smem_addr(&sh.sums_full[d]), d_phase);
-                if (!ok)
-                    break;
-                if (busy) {
-                    tcgen05_after_sync();
-                    // the next 32 sums are on their way while these are added
-                    const uint32_t from = mine + d * G_COLS;
-                    uint32_t p[2][32];
-                    tmem_ld32(from, p[0]);
+                for (int i = 0; i < 4; i++)
+                    c_row[i] = s_row[i];
+                if (b0 + 4 < g.kb)
+                    load_rows(b0 + 4);
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        tmem_wait_ld();
-                        if (q < 3)
-                            tmem_ld32(from + ((q + 1) >> 1) * 128 + ((q + 1) & 1) * 32,
-                                      p[(q + 1) & 1]);
-                        const float f = q >> 1 ? f1 : f0;
+                for (int i = 0; i < 4; i++) {
+                    if (b0 + i >= g.kb)
+                        break;
+                    const float f0 = c_row[i] * __shfl_sync(FULL_MASK, c_w0, b0 + i & 31);
+                    const float f1 = c_row[i] * __shfl_sync(FULL_MASK, c_w1, b0 + i & 31);
+                    if (!(ok = warp_wait(smem_addr(&sh.sums_full[d]), d_phase)))
+                        break;
+                    if (busy) {
+                        tcgen05_after_sync();
+                        // the next 32 sums are on their way while these are added
+                        const uint32_t from = mine + d * G_COLS;
+                        uint32_t p[2][32];
+                        tmem_ld32(from, p[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            float2 &c = acc[q >> 1][(q & 1) * 16 + i];
-                            c = fma2(make_float2(__uint_as_float(p[q & 1][2 * i]),
-                                                 __uint_as_float(p[q & 1][2 * i + 1])),
-                                     make_float2(f, f), c);
+                        for (int q = 0; q < 4; q++) {
+                            tmem_wait_ld();
+                            if (q < 3)
+                                tmem_ld32(from + ((q + 1) >> 1) * 128 + ((q + 1) & 1) * 32,
+                                          p[(q + 1) & 1]);
+                            const float f = q >> 1 ? f1 : f0;
+#pragma unroll
+                            for (int j = 0; j < 16; j++) {
+                                float2 &c = acc[q >> 1][(q & 1) * 16 + j];
+                                c = fma2(make_float2(__uint_as_float(p[q & 1][2 * j]),
+                                                     __uint_as_float(p[q & 1][2 * j + 1])),
+                                         make_float2(f, f), c);
+                            }
                         }
+                        tcgen05_before_sync();
                     }
-                    tcgen05_before_sync();
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.sums_empty[d]));
-                if (++d == 2) {
-                    d = 0;
-                    d_phase ^= 1;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sh.sums_empty[d]));
+                    d ^= 1;
+                    d_phase ^= d == 0;
                 }
             }
             if (!ok)
                 break;
-            if (tile + (int)gridDim.x < tiles) {  // its first scales load during the epilogue
-                next = gemm_tile(sh.seg, g, tile + gridDim.x);
+            if (unit + unit_step < units) {  // its first scales load during the epilogue
+                next = gemm_tile<CLUSTER>(sh.seg, g, unit + unit_step, rank);
                 open_tile(next);
             }
-            const int64_t n = t.row + r;
+            const int rows = t.store ? t.rows - quarter * 32 : 0;  // of the warp
+            const int64_t n = t.row + quarter * 32;
             if constexpr (OUT == OUT_SWIGLU) {
                 float amax = 0.0f;
 #pragma unroll
@@ -341,56 +425,48 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     break;
                 amax = fmaxf(amax, sh.amax[turn][half ^ 1][r]);
                 turn ^= 1;
-                if (r < t.rows) {
-                    float scale, inv;
-                    block_scale(amax, scale, inv);
-                    uint8_t *to = static_cast<uint8_t *>(g.out) + n * g.M + t.col * 128 + half * 64;
+                float scale, inv;
+                block_scale(amax, scale, inv);
+                uint32_t w[16];
 #pragma unroll
-                    for (int v = 0; v < 4; v++) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const float2 a = acc[0][v * 8 + 2 * i], b = acc[0][v * 8 + 2 * i + 1];
-                            w[i] = __nv_cvt_float2_to_fp8x2(
-                                       make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)),
-                                       __NV_SATFINITE, __NV_E4M3) |
-                                   (uint32_t)__nv_cvt_float2_to_fp8x2(
-                                       make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)),
-                                       __NV_SATFINITE, __NV_E4M3)
-                                       << 16;
-                        }
-                        st_v4(to + v * 16, make_uint4(w[0], w[1], w[2], w[3]));
-                    }
-                    if (half == 0)
-                        g.out_s[n * ob + t.col] = scale;
+                for (int i = 0; i < 16; i++) {
+                    const float2 a = acc[0][2 * i], b = acc[0][2 * i + 1];
+                    w[i] = __nv_cvt_float2_to_fp8x2(
+                               make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)),
+                               __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(
+                               make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)),
+                               __NV_SATFINITE, __NV_E4M3)
+                               << 16;
                 }
-            } else if (r < t.rows) {
+                store_rows(way, w,
+                           static_cast<uint8_t *>(g.out) + n * g.M + t.col * 128 + half * 64, g.M,
+                           64, rows);
+                if (half == 0 && lane < rows)
+                    g.out_s[(n + lane) * ob + t.col] = scale;
+            } else if (rows > 0) {
+                constexpr int SIZE = OUT == OUT_F32 ? 4 : 2;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int o = t.col * G_COLS + h * 128 + half * 64;
-                    if constexpr (OUT == OUT_F32) {
-                        float *to = static_cast<float *>(g.out) + n * g.M + o;
 #pragma unroll
-                        for (int v = 0; v < 16; v++)
-                            if (o + v * 4 < g.M)
-                                st_v4(to + v * 4,
-                                      make_uint4(__float_as_uint(acc[h][2 * v].x),
-                                                 __float_as_uint(acc[h][2 * v].y),
-                                                 __float_as_uint(acc[h][2 * v + 1].x),
-                                                 __float_as_uint(acc[h][2 * v + 1].y)));
-                    } else {
-                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(g.out) + n * g.M + o;
+                    for (int v = 0; v < SIZE; v++) {  // 64 bytes a row each
+                        uint32_t w[16];
 #pragma unroll
-                        for (int v = 0; v < 8; v++) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const __nv_bfloat162 b = __float22bfloat162_rn(acc[h][v * 4 + i]);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                        for (int i = 0; i < 16; i++) {
+                            if constexpr (OUT == OUT_F32) {
+                                const float2 c = acc[h][v * 8 + i / 2];
+                                w[i] = __float_as_uint(i & 1 ? c.y : c.x);
+                            } else {
+                                const __nv_bfloat162 c =
+                                    __float22bfloat162_rn(acc[h][v * 16 + i]);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&c);
                             }
-                            if (o + v * 8 < g.M)
-                                st_v4(to + v * 8, make_uint4(w[0], w[1], w[2], w[3]));
                         }
+                        const int at = o + v * (64 / SIZE);
+                        store_rows(way, w,
+                                   static_cast<uint8_t *>(g.out) + (n * g.M + at) * SIZE,
+                                   (int64_t)g.M * SIZE, (g.M - at) * SIZE, rows);
                     }
                 }
             }
@@ -400,15 +476,17 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         report(g.err_word, MOE_ERRBIT_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
+    if (CLUSTER > 1)
+        cluster_sync();  // nothing of the other's is on its way here
     if (warp == 9)
         tmem_free(tmem, 512);
 }
 
-template <int OUT, bool TRANS>
+template <int OUT, bool TRANS, int CLUSTER>
 cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uint8_t *w_q,
                      cudaStream_t stream)
 {
-    auto *kernel = expert_gemm_kernel<OUT, TRANS>;
+    auto *kernel = expert_gemm_kernel<OUT, TRANS, CLUSTER>;
     cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)G_SMEM);
     if (st != cudaSuccess)
@@ -427,7 +505,7 @@ cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uin
         args.halves = wide % 128 != 0;
         const MapDim dims[5] = {{args.halves ? wide : 128, 0, 128},
                                 {K, wide, 128},
-                                {args.halves ? 1 : wide / 128, 128, args.halves ? 1 : 2},
+                                {args.halves ? 1 : wide / 128, 128, args.halves || CLUSTER > 1 ? 1 : 2},
                                 {1, wide * K, 1},
                                 {g.E, wide * K, 1}};
         st = encode_map(&maps.w, type, w_q, dims);
@@ -435,8 +513,8 @@ cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uin
         // SwiGLU: gate and up; else 256 outputs
         const int64_t rows = OUT == OUT_SWIGLU ? g.M : wide, parts = wide / rows;
         const MapDim dims[5] = {{K, 0, 128},
-                                {rows, K, OUT == OUT_SWIGLU ? 128 : 256},
-                                {parts, rows * K, (int)parts},
+                                {rows, K, OUT == OUT_SWIGLU || CLUSTER > 1 ? 128 : 256},
+                                {parts, rows * K, CLUSTER > 1 ? 1 : (int)parts},
                                 {1, wide * K, 1},
                                 {g.E, wide * K, 1}};
         st = encode_map(&maps.w, type, w_q, dims);
@@ -445,8 +523,21 @@ cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uin
         return st;
     // no more CTAs than tiles can be (each expert may add one partial row tile)
     const int64_t most = ((int64_t)g.N / G_ROWS + (g.E < g.N ? g.E : g.N)) * g.col_tiles;
-    const int grid = (int)(most < sm_count() ? most : sm_count());
-    return launch_pdl(kernel, dim3(grid), dim3(G_THREADS), G_SMEM, stream, maps, args);
+    const int all = sm_count() / CLUSTER * CLUSTER;
+    const int grid = most < all ? (int)((most + CLUSTER - 1) / CLUSTER * CLUSTER) : all;
+    return launch_pdl_clusters(kernel, CLUSTER, dim3(grid), dim3(G_THREADS), G_SMEM, stream, maps,
+                               args);
+}
+
+template <int OUT, bool TRANS>
+cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uint8_t *w_q,
+                     cudaStream_t stream)
+{
+    // Pairs of row tiles share the weights' way through the L2 where experts have a
+    // tile's rows on average
+    if ((int64_t)g.N >= (int64_t)G_ROWS * g.E)
+        return run_gemm<OUT, TRANS, 2>(g, K, a_q, w_q, stream);
+    return run_gemm<OUT, TRANS, 1>(g, K, a_q, w_q, stream);
 }
 
 }  // namespace

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     if (warp == 9)
         tmem_alloc(smem_addr(&sh.tmem), 512);
     wait_prior_grid();
-    load_segments(sh.seg, g.offsets, g.E, g.N, 1, blockIdx.x == 0 ? g.err_word : nullptr);
+    load_segments(sh.seg, g.offsets, g.E, g.N, [](int) { return 0; },
+                  blockIdx.x == 0 ? g.err_word : nullptr);
     allow_next_grid();
     tcgen05_after_sync();
     const uint32_t tmem = sh.tmem;

@@ -18,17 +18,18 @@ __device__ __forceinline__ int2 segment(const int32_t *offsets, int e, int N, ui
     return make_int2(lo, hi);
 }
 
-// Every expert's first row, and the running count of row tiles before it.
+// Every expert's rows, and the running count of units of work before it.
 struct Segments {
     int lo[MOE_MAX_EXPERTS], hi[MOE_MAX_EXPERTS];
     int first[MOE_MAX_EXPERTS + 1];
 };
 
-// Fills s, in shared memory, for tiles of `step` rows; called by the whole CTA,
-// complete when it returns.  err_word: of one CTA, so that a fault is reported
-// once.
-__device__ inline void load_segments(Segments &s, const int32_t *offsets, int E, int N, int step,
-                                     uint32_t *err_word)
+// Fills s, in shared memory; units(rows): the units of a segment.  Called by the
+// whole CTA, complete when it returns.  err_word: of one CTA, so that a fault is
+// reported once.
+template <typename Units>
+__device__ inline void load_segments(Segments &s, const int32_t *offsets, int E, int N,
+                                     const Units &units, uint32_t *err_word)
 {
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int2 r = segment(offsets, e, N, err_word);
@@ -41,8 +42,8 @@ __device__ inline void load_segments(Segments &s, const int32_t *offsets, int E,
         int before = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const int tiles = e < E ? (s.hi[e] - s.lo[e] + step - 1) / step : 0;
-            int sum = tiles;
+            const int mine = e < E ? units(s.hi[e] - s.lo[e]) : 0;
+            int sum = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(FULL_MASK, sum, d);
@@ -50,7 +51,7 @@ __device__ inline void load_segments(Segments &s, const int32_t *offsets, int E,
                     sum += v;
             }
             if (e < E)
-                s.first[e] = before + sum - tiles;
+                s.first[e] = before + sum - mine;
             before += __shfl_sync(FULL_MASK, sum, 31);
         }
         if (lane == 0)
@@ -59,8 +60,8 @@ __device__ inline void load_segments(Segments &s, const int32_t *offsets, int E,
     __syncthreads();
 }
 
-// The expert whose row tiles hold number m (m < s.first[E]).
-__device__ __forceinline__ int expert_of_tile(const Segments &s, int E, int m)
+// The expert whose units hold number m (m < s.first[E]).
+__device__ __forceinline__ int expert_of_unit(const Segments &s, int E, int m)
 {
     int lo = 0, hi = E;  // first[lo] <= m < first[hi]
     while (hi - lo > 1) {

@@ -75,23 +75,32 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
-// The same for waits of a few hundred cycles that follow each other closely:
-// the timer, whose reading takes longer than such a wait, is looked at once in
-// 256 tries only.
+// mbar_try_wait that may leave the thread suspended for longer (up to `ns`), until
+// the phase completes: a warp that waits then takes no issue slots from the others.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return done != 0;
+}
+
+// mbar_wait in such tries, for waits that follow each other closely.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
 {
-    uint64_t t0 = 0;
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 256; i++)
-            if (mbar_try_wait(bar, parity))
-                return true;
-        const uint64_t t = global_ns();
-        if (t0 == 0)
-            t0 = t;
-        else if (t - t0 > MBAR_TIMEOUT_NS)
+    constexpr uint32_t TRY_NS = 1000000;
+    if (mbar_try_wait_for(bar, parity, TRY_NS))
+        return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait_for(bar, parity, TRY_NS))
+        if (global_ns() - t0 > MBAR_TIMEOUT_NS)
             return false;
-    }
+    return true;
 }
 
 // The same for a whole warp, whose lanes agree on the answer.
