@@ -138,30 +138,6 @@ __device__ __forceinline__ void weight_half(uint32_t wt, const CUtensorMap &map,
         tensor5_g2s(to, &map, x, y, z, 0, t.expert, bar);
 }
 
-// 64 bytes of each of a warp's rows, a row's with its lane, to global memory: rows side
-// by side in shared memory on the way, so that a store covers whole sectors.  `to` is
-// row 0's place; `bytes` are left of the row there, `rows` rows are there.
-__device__ __forceinline__ void store_rows(uint8_t *way, const uint32_t (&v)[16], uint8_t *to,
-                                           int64_t stride, int bytes, int rows)
-{
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        *reinterpret_cast<uint4 *>(way + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) =
-            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    __syncwarp();
-    const int piece = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = i * 8 + (lane >> 2);
-        const uint4 u =
-            *reinterpret_cast<const uint4 *>(way + r * 64 + (piece ^ (r >> 1 & 3)) * 16);
-        if (r < rows && piece * 16 < bytes)
-            st_v4(to + r * stride + piece * 16, u);
-    }
-}
-
 template <int OUT, bool TRANS, int CLUSTER>
 __global__ void __launch_bounds__(G_THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g)
@@ -206,9 +182,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     bool ok = true;  // false once one of this thread's waits gave up
 
     // the promotion warps hold 128 running sums a thread: the third warpgroup gives
-    // them its registers (168 at launch: 56 + 2 x 224 = 3 x 168)
+    // them its registers (168 at launch: 88 + 2 x 208 = 3 x 168)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             int s = 0;
             uint32_t phase = 0;
@@ -293,7 +269,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     ok = warp_wait(smem_addr(&sh.empty[i]), parity >> i & 1) && ok;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int half = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
@@ -392,9 +368,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         }
                         tcgen05_before_sync();
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&sh.sums_empty[d]));
+                    warp_arrive(smem_addr(&sh.sums_empty[d]));
                     d ^= 1;
                     d_phase ^= d == 0;
                 }
@@ -418,9 +392,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 }
                 // the block's other 64 channels are with the warp four on
                 sh.amax[turn][half][r] = amax;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.amax_full[quarter]));
+                warp_arrive(smem_addr(&sh.amax_full[quarter]));
                 if (!(ok = warp_wait(smem_addr(&sh.amax_full[quarter]), turn)))
                     break;
                 amax = fmaxf(amax, sh.amax[turn][half ^ 1][r]);

@@ -6,7 +6,8 @@
 // One persistent CTA per SM, 128 x 256 of one expert's dw a tile, 64 rows a stage:
 //   warps 0-7   read a chunk's sums from tensor memory into their running sums
 //               (thread: one o, 128 of the i), and store them after the last
-//   warp 8      tensor copies of dy and x, 64 rows x 64 columns each
+//   warp 8      tensor copies of dy and x, 64 rows each; in clusters of two, whose CTAs
+//               do neighbouring tiles of o, each brings half of x's columns to both
 //   warp 9      issues the MMAs, K = 16 rows each; rows behind the segment's end
 //               belong to the next expert and are zeroed in shared memory first
 // The tensor core's fp32 sum truncates: 2.1e-6 relative after 2048 rows, growing
@@ -33,6 +34,8 @@ constexpr int W_BOX = W_STEP * 128;  // bytes of 64 rows x 64 columns
 constexpr int W_BOXES = (W_M + W_K) / 64;
 constexpr int W_STAGE = W_BOXES * W_BOX;
 
+constexpr int W_OUT = 32 * 64;  // a warp's way out: 64 bytes of each of its rows
+
 struct WgradShared {
     uint64_t full[W_STAGES], empty[W_STAGES];
     uint64_t sums_full[2], sums_empty[2];
@@ -40,10 +43,13 @@ struct WgradShared {
     Segments seg;
 };
 
-constexpr size_t W_SMEM = 1024 + (size_t)W_STAGES * W_STAGE + sizeof(WgradShared);
+constexpr size_t W_SMEM =
+    1024 + (size_t)W_STAGES * W_STAGE + W_SUMS / 32 * W_OUT + sizeof(WgradShared);
+static_assert(W_SMEM <= 227 * 1024, "shared memory of one CTA");
 
 struct WgradArgs {
-    int N, M, K, E, m_tiles, k_tiles;
+    int N, M, K, E, m_tiles, k_tiles;  // m_tiles: a multiple of the cluster's CTAs
+    bool whole_m, whole_k;             // columns are whole boxes of 64: one copy for several
     const int32_t *offsets;
     float *dw;
     uint32_t *err_word;
@@ -53,19 +59,36 @@ struct WgradTile {
     int expert, lo, rows, m, k;
 };
 
-__device__ __forceinline__ WgradTile wgrad_tile(const Segments &s, const WgradArgs &g, int64_t tile)
+template <int CLUSTER>
+__device__ __forceinline__ WgradTile wgrad_tile(const Segments &s, const WgradArgs &g,
+                                                int64_t unit, int rank)
 {
     WgradTile t;
-    const int per = g.m_tiles * g.k_tiles;
-    t.expert = (int)(tile / per);
-    const int local = (int)(tile - (int64_t)t.expert * per);
-    t.m = local % g.m_tiles * W_M;
-    t.k = local / g.m_tiles * W_K;
+    const int m_units = g.m_tiles / CLUSTER, per = m_units * g.k_tiles;
+    t.expert = (int)(unit / per);
+    const int local = (int)(unit - (int64_t)t.expert * per);
+    t.m = (local % m_units * CLUSTER + rank) * W_M;
+    t.k = local / m_units * W_K;
     t.lo = s.lo[t.expert];
     t.rows = s.hi[t.expert] - t.lo;
     return t;
 }
 
+// `boxes` boxes of 64 columns from column `col` on, 64 rows from `row` on.
+template <bool MULTICAST>
+__device__ __forceinline__ void copy_columns(uint32_t to, const CUtensorMap &map, bool whole,
+                                             int boxes, int col, int row, uint32_t bar)
+{
+    for (int i = 0; i < (whole ? 1 : boxes); i++) {
+        const int x = whole ? 0 : col + i * 64, u = whole ? col / 64 : 0;
+        if (MULTICAST)
+            tensor5_g2s_multicast(to + i * W_BOX, &map, x, row, 0, u, 0, bar, 3);
+        else
+            tensor5_g2s(to + i * W_BOX, &map, x, row, 0, u, 0, bar);
+    }
+}
+
+template <int CLUSTER>
 __global__ void __launch_bounds__(W_THREADS, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy,
                         const __grid_constant__ CUtensorMap map_x, const WgradArgs g)
@@ -73,13 +96,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    WgradShared &sh = *reinterpret_cast<WgradShared *>(stages + W_STAGES * W_STAGE);
+    uint8_t *ways = stages + W_STAGES * W_STAGE;
+    WgradShared &sh = *reinterpret_cast<WgradShared *>(ways + W_SUMS / 32 * W_OUT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CLUSTER > 1 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < W_STAGES; i++) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), CLUSTER);  // the MMAs of all CTAs
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_addr(&sh.sums_full[i]), 1);
@@ -94,22 +119,25 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     wait_prior_grid();
     load_segments(sh.seg, g.offsets, g.E, g.N, [](int) { return 0; },
                   blockIdx.x == 0 ? g.err_word : nullptr);
+    if (CLUSTER > 1)
+        cluster_sync();  // the other's barriers are ready too
     allow_next_grid();
     tcgen05_after_sync();
     const uint32_t tmem = sh.tmem;
-    const int64_t tiles = (int64_t)g.E * g.m_tiles * g.k_tiles;
+    const int64_t units = (int64_t)g.E * (g.m_tiles / CLUSTER) * g.k_tiles;
+    const int first_unit = blockIdx.x / CLUSTER, unit_step = gridDim.x / CLUSTER;
     bool ok = true;  // false once one of this warp's waits gave up
 
     // the sums' warps hold 128 running sums a thread: the third warpgroup gives
-    // them its registers (168 at launch: 72 + 2 x 216 = 3 x 168)
+    // them its registers (168 at launch: 88 + 2 x 208 = 3 x 168)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-                const WgradTile t = wgrad_tile(sh.seg, g, tile);
+            for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+                const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
                 for (int n = 0; n < t.rows; n += W_STEP) {
                     if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
                         break;
@@ -117,13 +145,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     const uint32_t at = smem_addr(stages + s * W_STAGE);
                     if (elect_one()) {
                         mbar_arrive_expect_tx(bar, W_STAGE);
-#pragma unroll
-                        for (int i = 0; i < W_M / 64; i++)
-                            tensor_g2s(at + i * W_BOX, &map_dy, t.m + i * 64, t.lo + n, 0, bar);
-#pragma unroll
-                        for (int i = 0; i < W_K / 64; i++)
-                            tensor_g2s(at + (W_M / 64 + i) * W_BOX, &map_x, t.k + i * 64, t.lo + n,
-                                       0, bar);
+                        constexpr int SHARE = W_K / 64 / CLUSTER;  // of x's boxes
+                        const int first = rank * SHARE;
+                        copy_columns<(CLUSTER > 1)>(at + (W_M / 64 + first) * W_BOX, map_x,
+                                                    g.whole_k, SHARE, t.k + first * 64, t.lo + n,
+                                                    bar);
+                        copy_columns<false>(at, map_dy, g.whole_m, W_M / 64, t.m, t.lo + n, bar);
                     }
                     issued++;
                     if (++s == W_STAGES) {
@@ -144,8 +171,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             int s = 0, d = 0;
             uint32_t phase = 0, d_phase = 0;
             int64_t issued = 0;
-            for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-                const WgradTile t = wgrad_tile(sh.seg, g, tile);
+            for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+                const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
                 for (int n = 0; n < t.rows; n += W_STEP) {
                     const bool first = n % W_CHUNK == 0;
                     const int left = t.rows - n;
@@ -177,7 +204,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                                          !first || i > 0);
                         if (last)
                             tcgen05_commit(smem_addr(&sh.sums_full[d]));
-                        tcgen05_commit(smem_addr(&sh.empty[s]));
+                        if (CLUSTER > 1)
+                            tcgen05_commit_multicast(smem_addr(&sh.empty[s]), 3);
+                        else
+                            tcgen05_commit(smem_addr(&sh.empty[s]));
                     }
                     issued++;
                     if (++s == W_STAGES) {
@@ -195,13 +225,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 ok = warp_wait(smem_addr(&sh.empty[i % W_STAGES]), (i / W_STAGES) & 1) && ok;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int half = warp >> 2, quarter = warp & 3;
+        uint8_t *way = ways + warp * W_OUT;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
         int d = 0;
         uint32_t d_phase = 0;
-        for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-            const WgradTile t = wgrad_tile(sh.seg, g, tile);
+        for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+            const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; i++)
@@ -220,9 +251,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                         acc[q * 32 + i] += __uint_as_float(p[i]);
                 }
                 tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.sums_empty[d]));
+                warp_arrive(smem_addr(&sh.sums_empty[d]));
                 if (++d == 2) {
                     d = 0;
                     d_phase ^= 1;
@@ -230,16 +259,17 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             }
             if (!ok)
                 break;
-            const int m = t.m + quarter * 32 + lane, k = t.k + half * 128;
-            if (m < g.M) {
-                float *to = g.dw + ((int64_t)t.expert * g.M + m) * g.K + k;
+            const int m = t.m + quarter * 32, k = t.k + half * 128;
 #pragma unroll
-                for (int v = 0; v < 32; v++)
-                    if (k + v * 4 < g.K)
-                        st_v4(to + v * 4, make_uint4(__float_as_uint(acc[4 * v]),
-                                                     __float_as_uint(acc[4 * v + 1]),
-                                                     __float_as_uint(acc[4 * v + 2]),
-                                                     __float_as_uint(acc[4 * v + 3])));
+            for (int v = 0; v < 8; v++) {  // 64 bytes a row each
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    w[i] = __float_as_uint(acc[v * 16 + i]);
+                store_rows(way, w,
+                           reinterpret_cast<uint8_t *>(
+                               g.dw + ((int64_t)t.expert * g.M + m) * g.K + k + v * 16),
+                           (int64_t)g.K * 4, (g.K - k - v * 16) * 4, g.M - m);
             }
         }
     }
@@ -247,8 +277,50 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         report(g.err_word, MOE_ERRBIT_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
+    if (CLUSTER > 1)
+        cluster_sync();  // nothing of the other's is on its way here
     if (warp == 9)
         tmem_free(tmem, 512);
+}
+
+}  // namespace
+
+namespace {
+
+// Rows of `cols` bf16 in boxes of 64 rows x 64 columns, several side by side where the
+// columns are whole boxes.
+cudaError_t wgrad_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int boxes)
+{
+    const bool whole = cols % 64 == 0;
+    const MapDim dims[5] = {{whole ? 64 : cols, 0, 64},
+                            {rows, cols * 2, W_STEP},
+                            {1, cols * 2, 1},
+                            {whole ? cols / 64 : 1, whole ? 128 : cols * 2, whole ? boxes : 1},
+                            {1, cols * 2, 1}};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims);
+}
+
+template <int CLUSTER>
+cudaError_t run_wgrad(WgradArgs g, const void *dy, const void *x, cudaStream_t stream)
+{
+    auto *kernel = expert_wgrad_kernel<CLUSTER>;
+    cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)W_SMEM);
+    if (st != cudaSuccess)
+        return st;
+    CUtensorMap map_dy, map_x;
+    st = wgrad_map(&map_dy, dy, g.N, g.M, W_M / 64);
+    if (st == cudaSuccess)
+        st = wgrad_map(&map_x, x, g.N, g.K, W_K / 64 / CLUSTER);
+    if (st != cudaSuccess)
+        return st;
+    g.whole_m = g.M % 64 == 0;
+    g.whole_k = g.K % 64 == 0;
+    g.m_tiles = (g.m_tiles + CLUSTER - 1) / CLUSTER * CLUSTER;
+    const int64_t tiles = (int64_t)g.E * g.m_tiles * g.k_tiles;
+    const int all = sm_count() / CLUSTER * CLUSTER;
+    return launch_pdl_clusters(kernel, CLUSTER, dim3((unsigned)(tiles < all ? tiles : all)),
+                               dim3(W_THREADS), W_SMEM, stream, map_dy, map_x, g);
 }
 
 }  // namespace
@@ -259,23 +331,14 @@ cudaError_t launch_expert_wgrad(int N, int M, int K, int E, const void *dy, cons
 {
     if (N == 0)  // no rows, and nothing the tensor maps could describe
         return cudaMemsetAsync(dw, 0, (size_t)E * M * K * sizeof(float), stream);
-    cudaError_t st = cudaFuncSetAttribute(
-        expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W_SMEM);
-    if (st != cudaSuccess)
-        return st;
-    CUtensorMap map_dy, map_x;
-    st = encode_map(&map_dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, 1, N, M, W_STEP, 64);
-    if (st != cudaSuccess)
-        return st;
-    st = encode_map(&map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, 1, N, K, W_STEP, 64);
-    if (st != cudaSuccess)
-        return st;
-    const WgradArgs g = {N, M, K, E, (M + W_M - 1) / W_M, (K + W_K - 1) / W_K, offsets, dw,
-                         err_word};
-    const int64_t tiles = (int64_t)E * g.m_tiles * g.k_tiles;
-    const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-    return launch_pdl(expert_wgrad_kernel, dim3(grid), dim3(W_THREADS), W_SMEM, stream, map_dy,
-                      map_x, g);
+    const int m_tiles = (M + W_M - 1) / W_M;
+    const WgradArgs g = {N,     M,     K,       E,  m_tiles, (K + W_K - 1) / W_K,
+                         false, false, offsets, dw, err_word};
+    // pairs of tiles share x's way through the L2, unless too much of the last pair
+    // would lie behind M
+    if (m_tiles % 2 == 0 || m_tiles >= 5)
+        return run_wgrad<2>(g, dy, x, stream);
+    return run_wgrad<1>(g, dy, x, stream);
 }
 
 }  // namespace moe

@@ -600,9 +600,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                                 few_store<Act, DOWN, EACH>(act + (j0 + j) * PITCH, in_block, v);
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&sh.ready[s]));
+                        warp_arrive(smem_addr(&sh.ready[s]));
                     }
                     if (++s == stages) {
                         s = 0;
@@ -730,9 +728,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     }
                 }
                 if (take) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&sh.empty[s]));
+                    warp_arrive(smem_addr(&sh.empty[s]));
                 }
                 if (++s == stages) {
                     s = 0;
@@ -752,9 +748,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4 * NG; i++)
                         x[i * 32] = acc[i / 4][i % 4];
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&sh.given[in_pass]));
+                    warp_arrive(smem_addr(&sh.given[in_pass]));
                     continue;
                 }
                 if (!(ok = warp_wait(smem_addr(&sh.given[in_pass]), now)))
@@ -762,9 +756,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 4 * NG; i++)
                     acc[i / 4][i % 4] += x[i * 32];
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sh.taken[in_pass]));
+                warp_arrive(smem_addr(&sh.taken[in_pass]));
             }
 #pragma unroll
             for (int grp = 0; grp < NG; grp++) {

@@ -1,5 +1,5 @@
 // The experts' row segments, as the products' kernels cut them into tiles, and
-// the block quantisation of the products' epilogues.
+// what their epilogues share: stores by rows and the block quantisation.
 #pragma once
 
 #include "common.cuh"
@@ -72,6 +72,30 @@ __device__ __forceinline__ int expert_of_unit(const Segments &s, int E, int m)
             hi = mid;
     }
     return lo;
+}
+
+// 64 bytes of each of a warp's rows, a row's with its lane, to global memory: rows side
+// by side in shared memory on the way, so that a store covers whole sectors.  `to` is
+// row 0's place; `bytes` are left of the row there, `rows` rows are there.
+__device__ __forceinline__ void store_rows(uint8_t *way, const uint32_t (&v)[16], uint8_t *to,
+                                           int64_t stride, int bytes, int rows)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        *reinterpret_cast<uint4 *>(way + lane * 64 + (i ^ (lane >> 1 & 3)) * 16) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    __syncwarp();
+    const int piece = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 u =
+            *reinterpret_cast<const uint4 *>(way + r * 64 + (piece ^ (r >> 1 & 3)) * 16);
+        if (r < rows && piece * 16 < bytes)
+            st_v4(to + r * stride + piece * 16, u);
+    }
 }
 
 // Scale and reciprocal of a block whose largest magnitude is amax, each one

@@ -103,9 +103,25 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
     return true;
 }
 
-// The same for a whole warp, whose lanes agree on the answer.
+// The same for a whole warp, whose lanes agree on the answer.  The first tries stay
+// within one uniform branch.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "TRY_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+        "@p bra.uni DONE_%=;\n\t"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t"
+        "@q bra.uni TRY_%=;\n"
+        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done != 0)
+        return true;
     return __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
 }
 
@@ -117,6 +133,17 @@ __device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, ui
     if (__all_sync(0xffffffffu, a && b))
         return true;
     return warp_wait(bar_a, parity_a) && warp_wait(bar_b, parity_b);
+}
+
+// One arrival for a whole warp, without a branch.
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(threadIdx.x & 31)
+        : "memory");
 }
 
 // Global -> shared bulk copy of `bytes` (multiple of 16, both addresses
