@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *ways = stages + G_STAGES * G_STAGE;
     GemmShared &sh = *reinterpret_cast<GemmShared *>(ways + G_PROMOTE / 32 * G_OUT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = CLUSTER > 1 ? (int)cluster_rank() : 0;
     const int first_unit = blockIdx.x / CLUSTER, unit_step = gridDim.x / CLUSTER;
 
@@ -189,16 +189,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            for (int unit = first_unit; ok && unit < units; unit += unit_step) {
+            for (int unit = first_unit; unit < units; unit += unit_step) {
                 const GemmTile t = gemm_tile<CLUSTER>(sh.seg, g, unit, rank);
                 const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
                 const uint32_t bytes = (32 << box) * 128 + 2 * G_B_HALF;
                 for (int b = 0; b < g.kb; b++) {
-                    if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
-                        break;
+                    warp_wait(ok, smem_addr(&sh.empty[s]), phase ^ 1);
                     const uint32_t bar = smem_addr(&sh.full[s]);
                     const uint32_t at = smem_addr(stages + s * G_STAGE), wt = at + G_A_BYTES;
-                    if (elect_one()) {
+                    if (ok && elect_one()) {
                         mbar_arrive_expect_tx(bar, bytes);
                         if (CLUSTER > 1 && t.pair) {  // one half each, for both
                             weight_half<OUT, TRANS, true>(wt, maps.w, g, t, b, rank, bar);
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         }
                         tensor_g2s(at, &maps.a[box], b * 128, t.row, 0, bar);
                     }
-                    issued++;
+                    issued += ok;
                     if (++s == G_STAGES) {
                         s = 0;
                         phase ^= 1;
@@ -218,8 +217,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 }
             }
             // copies still in flight land before the CTA may end
+            bool landed = true;
             for (int64_t i = issued > G_STAGES ? issued - G_STAGES : 0; i < issued; i++)
-                ok = warp_wait(smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1) && ok;
+                warp_wait(landed, smem_addr(&sh.full[i % G_STAGES]), (i / G_STAGES) & 1);
+            ok = ok && landed;
         } else if (warp <= 10) {
             const uint32_t own = warp - 9;  // half of tensor memory, and parity of its stages
             constexpr uint32_t idesc = mma_desc(G_ROWS, G_COLS, 0, false, TRANS);
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const uint64_t b0 = smem_desc(base + G_A_BYTES, TRANS ? G_B_HALF : 16, 1024);
             int s = 0;
             uint32_t phase = 0, d_phase = 0, used = 0, parity = 0;
-            for (int unit = first_unit; ok && unit < units; unit += unit_step) {
+            for (int unit = first_unit; unit < units; unit += unit_step) {
                 for (int b = 0; b < g.kb; b++) {
                     const int at = s;
                     const uint32_t at_phase = phase;
@@ -241,14 +242,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     }
                     if ((at & 1) != own)
                         continue;
-                    if (!(ok = warp_wait2(smem_addr(&sh.sums_empty[own]), d_phase ^ 1,
-                                          smem_addr(&sh.full[at]), at_phase)))
-                        break;
+                    warp_wait2(ok, smem_addr(&sh.sums_empty[own]), d_phase ^ 1,
+                               smem_addr(&sh.full[at]), at_phase);
                     tcgen05_after_sync();
                     const uint64_t da = a0 + (uint32_t)(at * (G_STAGE >> 4));
                     const uint64_t db = b0 + (uint32_t)(at * (G_STAGE >> 4));
                     const uint32_t to = tmem + own * G_COLS;
-                    if (elect_one()) {
+                    if (ok && elect_one()) {
 #pragma unroll
                         for (int i = 0; i < 4; i++)
                             mma_f8(to, da + i * a_step, db + i * b_step, idesc, i > 0);
@@ -259,14 +259,16 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                             tcgen05_commit(smem_addr(&sh.empty[at]));
                     }
                     d_phase ^= 1;
-                    used |= 1u << at;
+                    used |= (uint32_t)ok << at;
                     parity = (parity & ~(1u << at)) | at_phase << at;
                 }
             }
             // and so do the MMAs' arrivals
+            bool done = true;
             for (int i = 0; i < G_STAGES; i++)
                 if (used >> i & 1)
-                    ok = warp_wait(smem_addr(&sh.empty[i]), parity >> i & 1) && ok;
+                    warp_wait(done, smem_addr(&sh.empty[i]), parity >> i & 1);
+            ok = ok && done;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             next = gemm_tile<CLUSTER>(sh.seg, g, first_unit, rank);
             open_tile(next);
         }
-        for (int unit = first_unit; ok && unit < units; unit += unit_step) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const GemmTile t = next;
             const bool busy = quarter * 32 < t.rows;  // of the warp
             float2 acc[2][32];
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             for (int i = 0; i < 32; i++)
                 acc[0][i] = acc[1][i] = make_float2(0.0f, 0.0f);
             float c_row[4], c_w0 = 0.0f, c_w1 = 0.0f;
-            for (int b0 = 0; ok && b0 < g.kb; b0 += 4) {
+            for (int b0 = 0; b0 < g.kb; b0 += 4) {
                 if ((b0 & 31) == 0) {
                     c_w0 = s_w0;
                     c_w1 = s_w1;
@@ -343,8 +345,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         break;
                     const float f0 = c_row[i] * __shfl_sync(FULL_MASK, c_w0, b0 + i & 31);
                     const float f1 = c_row[i] * __shfl_sync(FULL_MASK, c_w1, b0 + i & 31);
-                    if (!(ok = warp_wait(smem_addr(&sh.sums_full[d]), d_phase)))
-                        break;
+                    warp_wait(ok, smem_addr(&sh.sums_full[d]), d_phase);
                     if (busy) {
                         tcgen05_after_sync();
                         // the next 32 sums are on their way while these are added
@@ -373,8 +374,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     d_phase ^= d == 0;
                 }
             }
-            if (!ok)
-                break;
             if (unit + unit_step < units) {  // its first scales load during the epilogue
                 next = gemm_tile<CLUSTER>(sh.seg, g, unit + unit_step, rank);
                 open_tile(next);
@@ -393,8 +392,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 // the block's other 64 channels are with the warp four on
                 sh.amax[turn][half][r] = amax;
                 warp_arrive(smem_addr(&sh.amax_full[quarter]));
-                if (!(ok = warp_wait(smem_addr(&sh.amax_full[quarter]), turn)))
-                    break;
+                warp_wait(ok, smem_addr(&sh.amax_full[quarter]), turn);
                 amax = fmaxf(amax, sh.amax[turn][half ^ 1][r]);
                 turn ^= 1;
                 float scale, inv;

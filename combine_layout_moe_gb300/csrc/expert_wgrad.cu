@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *ways = stages + W_STAGES * W_STAGE;
     WgradShared &sh = *reinterpret_cast<WgradShared *>(ways + W_SUMS / 32 * W_OUT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = CLUSTER > 1 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
@@ -136,14 +136,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             int s = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+            for (int64_t unit = first_unit; unit < units; unit += unit_step) {
                 const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
                 for (int n = 0; n < t.rows; n += W_STEP) {
-                    if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
-                        break;
+                    warp_wait(ok, smem_addr(&sh.empty[s]), phase ^ 1);
                     const uint32_t bar = smem_addr(&sh.full[s]);
                     const uint32_t at = smem_addr(stages + s * W_STAGE);
-                    if (elect_one()) {
+                    if (ok && elect_one()) {
                         mbar_arrive_expect_tx(bar, W_STAGE);
                         constexpr int SHARE = W_K / 64 / CLUSTER;  // of x's boxes
                         const int first = rank * SHARE;
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                                                     bar);
                         copy_columns<false>(at, map_dy, g.whole_m, W_M / 64, t.m, t.lo + n, bar);
                     }
-                    issued++;
+                    issued += ok;
                     if (++s == W_STAGES) {
                         s = 0;
                         phase ^= 1;
@@ -160,8 +159,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 }
             }
             // copies still in flight land before the CTA may end
+            bool landed = true;
             for (int64_t i = issued > W_STAGES ? issued - W_STAGES : 0; i < issued; i++)
-                ok = warp_wait(smem_addr(&sh.full[i % W_STAGES]), (i / W_STAGES) & 1) && ok;
+                warp_wait(landed, smem_addr(&sh.full[i % W_STAGES]), (i / W_STAGES) & 1);
+            ok = ok && landed;
         } else if (warp == 9) {
             constexpr uint32_t idesc = mma_desc(W_M, W_K, 1, true, true);
             const uint32_t base = smem_addr(stages);
@@ -171,15 +172,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             int s = 0, d = 0;
             uint32_t phase = 0, d_phase = 0;
             int64_t issued = 0;
-            for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+            for (int64_t unit = first_unit; unit < units; unit += unit_step) {
                 const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
                 for (int n = 0; n < t.rows; n += W_STEP) {
                     const bool first = n % W_CHUNK == 0;
                     const int left = t.rows - n;
                     const bool last = left <= W_STEP || (n + W_STEP) % W_CHUNK == 0;
-                    if (!(ok = (!first || warp_wait(smem_addr(&sh.sums_empty[d]), d_phase ^ 1)) &&
-                               warp_wait(smem_addr(&sh.full[s]), phase)))
-                        break;
+                    if (first)
+                        warp_wait(ok, smem_addr(&sh.sums_empty[d]), d_phase ^ 1);
+                    warp_wait(ok, smem_addr(&sh.full[s]), phase);
                     tcgen05_after_sync();
                     const int steps = left < W_STEP ? (left + 15) / 16 : W_STEP / 16;
                     if (left < steps * 16) {
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     const uint64_t da = a0 + (uint32_t)(s * (W_STAGE >> 4));
                     const uint64_t db = b0 + (uint32_t)(s * (W_STAGE >> 4));
                     const uint32_t to = tmem + d * W_K;
-                    if (elect_one()) {
+                    if (ok && elect_one()) {
 #pragma unroll
                         for (int i = 0; i < W_STEP / 16; i++)
                             if (i < steps)
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                         else
                             tcgen05_commit(smem_addr(&sh.empty[s]));
                     }
-                    issued++;
+                    issued += ok;
                     if (++s == W_STAGES) {
                         s = 0;
                         phase ^= 1;
@@ -221,8 +222,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 }
             }
             // and so do the MMAs' arrivals
+            bool done = true;
             for (int64_t i = issued > W_STAGES ? issued - W_STAGES : 0; i < issued; i++)
-                ok = warp_wait(smem_addr(&sh.empty[i % W_STAGES]), (i / W_STAGES) & 1) && ok;
+                warp_wait(done, smem_addr(&sh.empty[i % W_STAGES]), (i / W_STAGES) & 1);
+            ok = ok && done;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -231,15 +234,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
         int d = 0;
         uint32_t d_phase = 0;
-        for (int64_t unit = first_unit; ok && unit < units; unit += unit_step) {
+        for (int64_t unit = first_unit; unit < units; unit += unit_step) {
             const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; i++)
                 acc[i] = 0.0f;
             for (int n = 0; n < t.rows; n += W_CHUNK) {
-                if (!(ok = warp_wait(smem_addr(&sh.sums_full[d]), d_phase)))
-                    break;
+                warp_wait(ok, smem_addr(&sh.sums_full[d]), d_phase);
                 tcgen05_after_sync();
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
@@ -257,8 +259,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     d_phase ^= 1;
                 }
             }
-            if (!ok)
-                break;
             const int m = t.m + quarter * 32, k = t.k + half * 128;
 #pragma unroll
             for (int v = 0; v < 8; v++) {  // 64 bytes a row each

@@ -77,7 +77,6 @@ struct FewShared {
     uint8_t token[MOE_FEW_MAX_PAIRS];      // token of each row
     int16_t pos[MOE_MAX_EXPERTS];          // first entry of e
     int active, longest, last;
-    int failed;                            // a wait gave up
 };
 
 // Weights in boxes of 1, 2, 4 and 8 tiles' rows and two blocks.  Five dimensions: 128
@@ -253,7 +252,6 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
         }
         longest = min(longest, FEW_ROWS);
         if (lane == 0) {
-            s.failed = 0;
             s.row0[n] = rows;
             s.active = n;
             s.longest = longest;
@@ -457,7 +455,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // each warp the sums of 16 outputs x T tokens
     float *sums = reinterpret_cast<float *>(top - sizeof(FewShared)) -
                   (DOWN ? FEW_WARPS * 16 * g.T : FEW_TILES * GIVEN);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int K = DOWN ? g.I : g.H;
     const int blocks = (K + TY::KB - 1) / TY::KB;
 
@@ -511,7 +509,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     uint32_t used = 0, parity = 0;  // a loader's slots that it filled, and their last phase
     bool ok = true;       // false once one of this warp's waits gave up
 
-    for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
+    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
         Work work = whole;
         if (DOWN) {
             const int group = job / whole.shares;
@@ -527,7 +525,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             constexpr int WORDS = DOWN ? EACH : EACH / 2;
             constexpr int BATCH = 4;               // tokens in flight
             const int block = lane >> 4, in_block = (lane & 15) * EACH;
-            while (ok && work.q < work.end) {
+            while (work.q < work.end) {
                 const Pass p = next_pass<DOWN>(work);
                 const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
                 const int wrow = p.tile * (DOWN ? 16 : 8);
@@ -544,11 +542,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                             }
                         };
                         load(0);  // in flight during the wait
-                        if (!(ok = warp_wait(smem_addr(&sh.empty[s]), phase ^ 1)))
-                            break;
+                        warp_wait(ok, smem_addr(&sh.empty[s]), phase ^ 1);
                         const uint32_t bar = smem_addr(&sh.full[s]);
                         uint8_t *stage = ring + s * stage_bytes;
-                        if (elect_one()) {
+                        if (ok && elect_one()) {
                             mbar_arrive_expect_tx(bar, 2 * p.tiles * FEW_TILE);
                             int done = 0;  // tiles, in boxes of falling size
 #pragma unroll
@@ -568,7 +565,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                             }
                         }
                         __syncwarp();
-                        used |= 1u << s;
+                        used |= (uint32_t)ok << s;
                         parity = (parity & ~(1u << s)) | phase << s;
                         float *factors =
                             reinterpret_cast<float *>(stage + w_bytes) + block * FEW_ROWS;
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         const int r8 = lane >> 2, c4 = lane & 3;  // this lane's row (and row + 8) and columns
         const int slice = warp / per, in_pass = warp - slice * per;
         const bool member = slice < slices;
-        while (ok && work.q < work.end) {
+        while (work.q < work.end) {
             const Pass p = next_pass<DOWN>(work);
             const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
             const bool busy = member && in_pass < p.tiles;
@@ -664,9 +661,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                         v_lo = s_lo[at];
                         v_hi = s_hi[at];
                     }
-                    if (!(ok = warp_wait2(smem_addr(&sh.ready[s]), phase, smem_addr(&sh.full[s]),
-                                          phase)))
-                        break;
+                    warp_wait2(ok, smem_addr(&sh.ready[s]), phase, smem_addr(&sh.full[s]), phase);
                 }
                 if (take && busy && b < blocks) {
                     const uint8_t *stage = ring + s * stage_bytes;
@@ -735,24 +730,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     phase ^= 1;
                 }
             }
-            if (!ok)
-                break;
             if (!busy)
                 continue;
             if (!DOWN) {  // the two slices' sums meet
                 float *x = sums + in_pass * GIVEN + lane;
                 const uint32_t now = meetings++ & 1;
                 if (slice == 1) {
-                    if (!(ok = warp_wait(smem_addr(&sh.taken[in_pass]), now ^ 1)))
-                        break;
+                    warp_wait(ok, smem_addr(&sh.taken[in_pass]), now ^ 1);
 #pragma unroll
                     for (int i = 0; i < 4 * NG; i++)
                         x[i * 32] = acc[i / 4][i % 4];
                     warp_arrive(smem_addr(&sh.given[in_pass]));
                     continue;
                 }
-                if (!(ok = warp_wait(smem_addr(&sh.given[in_pass]), now)))
-                    break;
+                warp_wait(ok, smem_addr(&sh.given[in_pass]), now);
 #pragma unroll
                 for (int i = 0; i < 4 * NG; i++)
                     acc[i / 4][i % 4] += x[i * 32];
@@ -781,13 +772,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
 
         if (DOWN) {
-            if (!ok)
-                sh.failed = 1;
             named_barrier(1, 32 * FEW_WARPS);  // every warp's sums are complete
-            if (sh.failed) {                   // and no warp waits for one that has left
-                ok = false;
-                continue;
-            }
             // the slices of a tile, added up by its first warp
             const int o = (work.tile + warp) * 16 + (lane & 15);
             const bool mine = warp < work.tiles && o < g.H;
@@ -831,9 +816,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
     }
     // copies still in flight land before the CTA may end
+    bool landed = true;
     for (int i = 0; warp >= FEW_WARPS && i < stages; i++)
         if (used >> i & 1)
-            ok = warp_wait(smem_addr(&sh.full[i]), parity >> i & 1) && ok;
+            warp_wait(landed, smem_addr(&sh.full[i]), parity >> i & 1);
+    ok = ok && landed;
     if (!ok)
         report(g.err_word, MOE_ERRBIT_TIMEOUT);
 }

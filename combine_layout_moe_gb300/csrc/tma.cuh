@@ -103,9 +103,18 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity)
     return true;
 }
 
-// The same for a whole warp, whose lanes agree on the answer.  The first tries stay
-// within one uniform branch.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+// This thread's warp in its CTA, in a form that the compiler knows to be the same for
+// the whole warp.
+__device__ __forceinline__ int warp_index()
+{
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+
+// The same for a whole warp, whose lanes agree on the answer; no wait at all once `ok`
+// is false, which ends true as long as none has given up.  Loops around such waits run
+// on in any case, doing nothing, so that their control does not depend on `ok` and
+// their addresses and descriptors stay in uniform registers.
+__device__ __forceinline__ void warp_wait(bool &ok, uint32_t bar, uint32_t parity)
 {
     uint32_t done;
     asm volatile(
@@ -114,25 +123,25 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "vote.sync.all.pred p, p, 0xffffffff;\n\t"
         "@p bra.uni DONE_%=;\n\t"
-        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, %3;\n\t"
         "@q bra.uni TRY_%=;\n"
         "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(ok ? 256u : 0u)
         : "memory");
-    if (done != 0)
-        return true;
-    return __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
+    if (done == 0 && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
 }
 
 // For two barriers; the answers of both first tries are awaited together.
-__device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b,
-                                           uint32_t parity_b)
+__device__ __forceinline__ void warp_wait2(bool &ok, uint32_t bar_a, uint32_t parity_a,
+                                           uint32_t bar_b, uint32_t parity_b)
 {
     const bool a = mbar_try_wait(bar_a, parity_a), b = mbar_try_wait(bar_b, parity_b);
     if (__all_sync(0xffffffffu, a && b))
-        return true;
-    return warp_wait(bar_a, parity_a) && warp_wait(bar_b, parity_b);
+        return;
+    warp_wait(ok, bar_a, parity_a);
+    warp_wait(ok, bar_b, parity_b);
 }
 
 // One arrival for a whole warp, without a branch.
