@@ -8,8 +8,9 @@
 // row by any fp32 factor, so the tensor core cannot sum over blocks: it
 // multiplies one block (four tcgen05.mma of K = 32 into tensor memory), and the
 // promotion warps read the 128 x 256 fp32 sums back, scale them and add them to
-// the running sums in their registers (one packed fused multiply-add for two
-// outputs) while the tensor core fills the other half of tensor memory.
+// the running sums in their registers while the tensor core fills the other half of
+// tensor memory.  (Plain fused multiply-adds: the packed ones take half of the issue
+// slots, but run on one of the two fp32 pipes alone, 512 cycles a block instead of 256.)
 //
 // One persistent CTA per SM, 128 rows x 256 outputs a tile:
 //   warps 0-7   promotion: warp w holds rows 32 (w % 4) .. +31, a thread one
@@ -322,10 +323,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         for (int unit = first_unit; unit < units; unit += unit_step) {
             const GemmTile t = next;
             const bool busy = quarter * 32 < t.rows;  // of the warp
-            float2 acc[2][32];
+            float acc[2][64];
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-                acc[0][i] = acc[1][i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 64; i++)
+                acc[0][i] = acc[1][i] = 0.0f;
             float c_row[4], c_w0 = 0.0f, c_w1 = 0.0f;
             for (int b0 = 0; b0 < g.kb; b0 += 4) {
                 if ((b0 & 31) == 0) {
@@ -350,21 +351,16 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         tcgen05_after_sync();
                         // the next 32 sums are on their way while these are added
                         const uint32_t from = mine + d * G_COLS;
-                        uint32_t p[2][32];
-                        tmem_ld32(from, p[0]);
+                        uint32_t p[1][32];
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
+                            tmem_ld32(from + (q >> 1) * 128 + (q & 1) * 32, p[0]);
                             tmem_wait_ld();
-                            if (q < 3)
-                                tmem_ld32(from + ((q + 1) >> 1) * 128 + ((q + 1) & 1) * 32,
-                                          p[(q + 1) & 1]);
                             const float f = q >> 1 ? f1 : f0;
 #pragma unroll
-                            for (int j = 0; j < 16; j++) {
-                                float2 &c = acc[q >> 1][(q & 1) * 16 + j];
-                                c = fma2(make_float2(__uint_as_float(p[q & 1][2 * j]),
-                                                     __uint_as_float(p[q & 1][2 * j + 1])),
-                                         make_float2(f, f), c);
+                            for (int j = 0; j < 32; j++) {
+                                float &c = acc[q >> 1][(q & 1) * 32 + j];
+                                c = fmaf(__uint_as_float(p[0][j]), f, c);
                             }
                         }
                         tcgen05_before_sync();
@@ -383,11 +379,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if constexpr (OUT == OUT_SWIGLU) {
                 float amax = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    const float2 v = acc[0][i];
-                    acc[0][i].x = v.x / (1.0f + expf(-v.x)) * acc[1][i].x;
-                    acc[0][i].y = v.y / (1.0f + expf(-v.y)) * acc[1][i].y;
-                    amax = fmaxf(amax, fmaxf(fabsf(acc[0][i].x), fabsf(acc[0][i].y)));
+                for (int i = 0; i < 64; i++) {
+                    const float v = acc[0][i];
+                    acc[0][i] = v / (1.0f + expf(-v)) * acc[1][i];
+                    amax = fmaxf(amax, fabsf(acc[0][i]));
                 }
                 // the block's other 64 channels are with the warp four on
                 sh.amax[turn][half][r] = amax;
@@ -400,12 +395,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
-                    const float2 a = acc[0][2 * i], b = acc[0][2 * i + 1];
+                    const float *h = &acc[0][4 * i];
                     w[i] = __nv_cvt_float2_to_fp8x2(
-                               make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)),
+                               make_float2(__fmul_rn(h[0], inv), __fmul_rn(h[1], inv)),
                                __NV_SATFINITE, __NV_E4M3) |
                            (uint32_t)__nv_cvt_float2_to_fp8x2(
-                               make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)),
+                               make_float2(__fmul_rn(h[2], inv), __fmul_rn(h[3], inv)),
                                __NV_SATFINITE, __NV_E4M3)
                                << 16;
                 }
@@ -425,11 +420,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
                             if constexpr (OUT == OUT_F32) {
-                                const float2 c = acc[h][v * 8 + i / 2];
-                                w[i] = __float_as_uint(i & 1 ? c.y : c.x);
+                                w[i] = __float_as_uint(acc[h][v * 16 + i]);
                             } else {
-                                const __nv_bfloat162 c =
-                                    __float22bfloat162_rn(acc[h][v * 16 + i]);
+                                const __nv_bfloat162 c = __floats2bfloat162_rn(
+                                    acc[h][v * 32 + 2 * i], acc[h][v * 32 + 2 * i + 1]);
                                 w[i] = *reinterpret_cast<const uint32_t *>(&c);
                             }
                         }
