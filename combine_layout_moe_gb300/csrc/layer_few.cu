@@ -459,7 +459,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     const int K = DOWN ? g.I : g.H;
     const int blocks = (K + TY::KB - 1) / TY::KB;
 
-    wait_prior_grid();
+    // DOWN starts while UP still runs elsewhere: the ids and the weights were there before
+    // UP (which waited for what made them), h and the counters are waited for below
+    if (!DOWN)
+        wait_prior_grid();
     allow_next_grid();
     if (!DOWN) {  // the second kernel's counters
         const int i = blockIdx.x * FEW_THREADS + threadIdx.x;
@@ -541,7 +544,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                                                      K);
                             }
                         };
-                        load(0);  // in flight during the wait
+                        if (!DOWN || used != 0)
+                            load(0);  // in flight during the wait
                         warp_wait(ok, smem_addr(&sh.empty[s]), phase ^ 1);
                         const uint32_t bar = smem_addr(&sh.full[s]);
                         uint8_t *stage = ring + s * stage_bytes;
@@ -565,6 +569,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                             }
                         }
                         __syncwarp();
+                        if (DOWN && used == 0) {
+                            wait_prior_grid();
+                            load(0);
+                        }
                         used |= (uint32_t)ok << s;
                         parity = (parity & ~(1u << s)) | phase << s;
                         float *factors =
@@ -609,6 +617,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
 
         if (DOWN) {
+            wait_prior_grid();
             named_barrier(1, 32 * FEW_WARPS);  // the job before has been read
             for (int i = lane; i < 16 * g.T; i += 32)
                 sums[warp * 16 * g.T + i] = 0.0f;
