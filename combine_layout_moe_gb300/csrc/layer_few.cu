@@ -115,14 +115,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
-    return v;
-}
 
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
 {
@@ -440,7 +432,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 {
     using TY = FewType<W>;
     constexpr bool FP8 = sizeof(W) == 1;
-    constexpr int CHAINS = DOWN ? 4 : 2;  // sums that do not wait for each other
+    // columns of a group: UP eight tokens; DOWN four, both terms of each side by side, so
+    // that a lane gets both and adds them
+    constexpr int GROUP = DOWN ? 4 : 8, GROUPS = NG * 8 / GROUP, SUMS = DOWN ? 2 : 4;
     using Act = typename TY::Act;
     // bytes of a row of activations in a block, padded so that the rows of a group
     // start in different banks: 4 inputs of both terms are 16 bytes, of one term 8
@@ -642,7 +636,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             const uint32_t tile_at = before * 2 * FEW_TILE + (slice & 1) * (FEW_TILE << box) +
                                      (in_pass - before) * (DOWN ? 2048 : 1024) +
                                      ((lane >> 3) & 1) * half_step + (lane & 7) * 128;
-            const uint32_t act_offset = act_at + (slice & 1) * act_block + r8 * PITCH + c4 * (DOWN ? 16 : 8);
+            const uint32_t act_offset =
+                act_at + (slice & 1) * act_block +
+                (DOWN ? (r8 >> 1) * PITCH + c4 * 16 + (r8 & 1) * 8 : r8 * PITCH + c4 * 8);
             const float *s_lo = nullptr, *s_hi = nullptr;  // of rows 0-7 and 8-15
             float v_lo = 0.0f, v_hi = 0.0f;
             if (FP8 && busy) {
@@ -654,11 +650,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     s_hi = s_lo + (int64_t)(g.I / 128) * blocks;
                 }
             }
-            float acc[NG][4];
+            float acc[GROUPS][SUMS];
 #pragma unroll
-            for (int i = 0; i < NG; i++) {
-                acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-            }
+            for (int i = 0; i < GROUPS; i++)
+#pragma unroll
+                for (int c = 0; c < SUMS; c++)
+                    acc[i][c] = 0.0f;
             for (int b0 = 0, mine = 0; b0 < blocks; b0 += 2) {
                 const bool take = member && turn == slice >> 1;
                 if (++turn == teams)
@@ -699,34 +696,36 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     mine++;
                     const uint32_t act = smem_addr(stage) + act_offset;
 #pragma unroll
-                    for (int grp = 0; grp < NG; grp++) {
-                        if (grp * 8 < n) {
-                            float part[CHAINS][4] = {};
-                            const uint32_t row = act + grp * 8 * PITCH;
+                    for (int grp = 0; grp < GROUPS; grp++) {
+                        if (grp * GROUP < n) {
+                            float part[2][4] = {};  // sums that do not wait for each other
+                            const uint32_t row = act + grp * GROUP * PITCH;
 #pragma unroll
                             for (int j = 0; j < TY::STEPS; j++) {
-                                if (DOWN) {
-                                    const uint4 v = lds128(row + j * 64);
-                                    mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
-                                    mma_16816(Act(), part[2 + (j & 1) & CHAINS - 1], a[j], v.z, v.w);
-                                } else {
-                                    const uint2 v = lds64(row + j * 32);
-                                    mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
-                                }
+                                const uint2 v = lds64(row + j * (DOWN ? 64 : 32));
+                                mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
                             }
-                            float2 back = make_float2(1.0f, 1.0f);  // the columns' powers of two
-                            if (FP8)
-                                back = *reinterpret_cast<const float2 *>(
-                                    stage + w_bytes +
-                                    ((slice & 1) * FEW_ROWS + grp * 8 + c4 * 2) * 4);
+                            // the columns' powers of two
+                            const float *back = reinterpret_cast<const float *>(stage + w_bytes) +
+                                                (slice & 1) * FEW_ROWS + grp * GROUP;
+                            if constexpr (DOWN) {
+                                const float f = FP8 ? back[c4] : 1.0f;
+                                acc[grp][0] = fmaf((part[0][0] + part[1][0]) +
+                                                       (part[0][1] + part[1][1]),
+                                                   f_lo * f, acc[grp][0]);
+                                acc[grp][1] = fmaf((part[0][2] + part[1][2]) +
+                                                       (part[0][3] + part[1][3]),
+                                                   f_hi * f, acc[grp][1]);
+                            } else {
+                                float2 f = make_float2(1.0f, 1.0f);
+                                if (FP8)
+                                    f = *reinterpret_cast<const float2 *>(back + c4 * 2);
 #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                float v = part[0][i] + part[1][i];
-                                if (DOWN)
-                                    v += part[CHAINS - 2][i] + part[CHAINS - 1][i];
-                                acc[grp][i] = fmaf(
-                                    v, (i < 2 ? f_lo : f_hi) * (i & 1 ? back.y : back.x),
-                                    acc[grp][i]);
+                                for (int i = 0; i < 4; i++)
+                                    acc[grp][i] = fmaf(part[0][i] + part[1][i],
+                                                       (i < 2 ? f_lo : f_hi) *
+                                                           (i & 1 ? f.y : f.x),
+                                                       acc[grp][i]);
                             }
                         }
                     }
@@ -741,7 +740,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             }
             if (!busy)
                 continue;
-            if (!DOWN) {  // the two slices' sums meet
+            if constexpr (!DOWN) {  // the two slices' sums meet
                 float *x = sums + in_pass * GIVEN + lane;
                 const uint32_t now = meetings++ & 1;
                 if (slice == 1) {
@@ -758,23 +757,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     acc[i / 4][i % 4] += x[i * 32];
                 warp_arrive(smem_addr(&sh.taken[in_pass]));
             }
+            if constexpr (DOWN) {
 #pragma unroll
-            for (int grp = 0; grp < NG; grp++) {
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int col = grp * 8 + c4 * 2 + i;
-                    if (col >= n)
-                        continue;
-                    if (DOWN) {
+                for (int grp = 0; grp < GROUPS; grp++) {
+                    const int col = grp * GROUP + c4;
+                    if (col < n) {
                         float *to = sums + (warp * g.T + sh.token[row0 + col]) * 16 + r8;
-                        to[0] += acc[grp][i];
-                        to[8] += acc[grp][2 + i];
-                        continue;
+                        to[0] += acc[grp][0];
+                        to[8] += acc[grp][1];
                     }
-                    const float gate = acc[grp][i];
-                    const float v =
-                        gate / (1.0f + expf(-gate)) * acc[grp][2 + i] * sh.w[row0 + col];
-                    g.h[(int64_t)(row0 + col) * g.I + tile * 8 + r8] = v;
+                }
+            } else {
+#pragma unroll
+                for (int grp = 0; grp < GROUPS; grp++) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int col = grp * GROUP + c4 * 2 + i;
+                        if (col >= n)
+                            continue;
+                        const float gate = acc[grp][i];
+                        g.h[(int64_t)(row0 + col) * g.I + tile * 8 + r8] =
+                            gate / (1.0f + expf(-gate)) * acc[grp][2 + i] * sh.w[row0 + col];
+                    }
                 }
             }
             __syncwarp();
