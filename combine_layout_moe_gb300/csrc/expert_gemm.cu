@@ -243,8 +243,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     }
                     if ((at & 1) != own)
                         continue;
-                    warp_wait2(ok, smem_addr(&sh.sums_empty[own]), d_phase ^ 1,
-                               smem_addr(&sh.full[at]), at_phase);
+                    // the block is there long before the sums are free: waited for first, it
+                    // adds nothing
+                    warp_wait(ok, smem_addr(&sh.full[at]), at_phase);
+                    warp_wait(ok, smem_addr(&sh.sums_empty[own]), d_phase ^ 1);
                     tcgen05_after_sync();
                     const uint64_t da = a0 + (uint32_t)(at * (G_STAGE >> 4));
                     const uint64_t db = b0 + (uint32_t)(at * (G_STAGE >> 4));
@@ -351,21 +353,31 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         tcgen05_after_sync();
                         // the next 32 sums are on their way while these are added
                         const uint32_t from = mine + d * G_COLS;
-                        uint32_t p[1][32];
+                        uint32_t p[2][32];
+                        tmem_ld32(from, p[0]);
+                        tmem_ld32(from + 32, p[1]);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
-                            tmem_ld32(from + (q >> 1) * 128 + (q & 1) * 32, p[0]);
-                            tmem_wait_ld();
+                            if (q == 2) {
+ tmem_ld32(from + 128, p[0]);
+ tmem_ld32(from + 160, p[1]);
+ tmem_wait_ld();
+}
+                            if (q == 2) {
+                                tcgen05_before_sync();
+                                warp_arrive(smem_addr(&sh.sums_empty[d]));
+                            }
                             const float f = q >> 1 ? f1 : f0;
 #pragma unroll
                             for (int j = 0; j < 32; j++) {
                                 float &c = acc[q >> 1][(q & 1) * 32 + j];
-                                c = fmaf(__uint_as_float(p[0][j]), f, c);
+                                c = fmaf(__uint_as_float(p[q & 1][j]), f, c);
                             }
                         }
-                        tcgen05_before_sync();
+                    } else {
+                        warp_arrive(smem_addr(&sh.sums_empty[d]));
                     }
-                    warp_arrive(smem_addr(&sh.sums_empty[d]));
                     d ^= 1;
                     d_phase ^= d == 0;
                 }

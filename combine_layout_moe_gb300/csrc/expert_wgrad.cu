@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             constexpr uint32_t k_step = 16 * 128 >> 4;  // sixteen rows on
             int s = 0, d = 0;
             uint32_t phase = 0, d_phase = 0;
+            bool ready = false;  // the stage was there when the one before was issued
             int64_t issued = 0;
             for (int64_t unit = first_unit; unit < units; unit += unit_step) {
                 const WgradTile t = wgrad_tile<CLUSTER>(sh.seg, g, unit, rank);
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     const bool last = left <= W_STEP || (n + W_STEP) % W_CHUNK == 0;
                     if (first)
                         warp_wait(ok, smem_addr(&sh.sums_empty[d]), d_phase ^ 1);
-                    warp_wait(ok, smem_addr(&sh.full[s]), phase);
+                    if (!__all_sync(FULL_MASK, ready))
+                        warp_wait(ok, smem_addr(&sh.full[s]), phase);
                     tcgen05_after_sync();
                     const int steps = left < W_STEP ? (left + 15) / 16 : W_STEP / 16;
                     if (left < steps * 16) {
@@ -197,6 +199,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     const uint64_t da = a0 + (uint32_t)(s * (W_STAGE >> 4));
                     const uint64_t db = b0 + (uint32_t)(s * (W_STAGE >> 4));
                     const uint32_t to = tmem + d * W_K;
+                    const int after = s + 1 == W_STAGES ? 0 : s + 1;
+                    ready = mbar_test(smem_addr(&sh.full[after]), phase ^ (after == 0));
                     if (ok && elect_one()) {
 #pragma unroll
                         for (int i = 0; i < W_STEP / 16; i++)
