@@ -31,6 +31,21 @@ int sm_count()
     return n;
 }
 
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &allowed)
+{
+    int dev = 0;
+    cudaError_t st = cudaGetDevice(&dev);
+    if (st != cudaSuccess)
+        return st;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (allowed.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (st == cudaSuccess)
+        allowed.fetch_or(bit, std::memory_order_release);
+    return st;
+}
+
 int warp_item_grid(const void *kernel, int threads, size_t smem, int64_t items)
 {
     int per_sm = 0;

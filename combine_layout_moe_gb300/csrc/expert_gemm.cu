@@ -91,13 +91,14 @@ __device__ __forceinline__ int gemm_units(int rows, int cols)
     return CLUSTER == 1 ? tiles * cols : tiles / 2 * cols + (tiles & 1) * ((cols + 1) / 2);
 }
 
-// Row tiles vary fastest: neighbours in time share the expert's weights.
+// Row tiles vary fastest: neighbours in time share the expert's weights.  `from`: the
+// expert of an earlier unit.
 template <int CLUSTER>
 __device__ __forceinline__ GemmTile gemm_tile(const Segments &s, const GemmArgs &g, int unit,
-                                              int rank)
+                                              int rank, int from)
 {
     GemmTile t;
-    t.expert = expert_of_unit(s, g.E, unit);
+    t.expert = expert_of_unit(s, unit, from);
     const int lo = s.lo[t.expert], hi = s.hi[t.expert];
     const int tiles = (hi - lo + G_ROWS - 1) / G_ROWS;
     int local = unit - s.first[t.expert], m;
@@ -187,11 +188,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
-            int s = 0;
+            int s = 0, expert = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
             for (int unit = first_unit; unit < units; unit += unit_step) {
-                const GemmTile t = gemm_tile<CLUSTER>(sh.seg, g, unit, rank);
+                const GemmTile t = gemm_tile<CLUSTER>(sh.seg, g, unit, rank, expert);
+                expert = t.expert;
                 const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
                 const uint32_t bytes = (32 << box) * 128 + 2 * G_B_HALF;
                 for (int b = 0; b < g.kb; b++) {
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         uint32_t d_phase = 0, turn = 0;
         GemmTile next;
         if (first_unit < units) {
-            next = gemm_tile<CLUSTER>(sh.seg, g, first_unit, rank);
+            next = gemm_tile<CLUSTER>(sh.seg, g, first_unit, rank, 0);
             open_tile(next);
         }
         for (int unit = first_unit; unit < units; unit += unit_step) {
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 }
             }
             if (unit + unit_step < units) {  // its first scales load during the epilogue
-                next = gemm_tile<CLUSTER>(sh.seg, g, unit + unit_step, rank);
+                next = gemm_tile<CLUSTER>(sh.seg, g, unit + unit_step, rank, t.expert);
                 open_tile(next);
             }
             const int rows = t.store ? t.rows - quarter * 32 : 0;  // of the warp
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 64; i++) {
                     const float v = acc[0][i];
-                    acc[0][i] = v / (1.0f + expf(-v)) * acc[1][i];
+                    acc[0][i] = silu(v) * acc[1][i];
                     amax = fmaxf(amax, fabsf(acc[0][i]));
                 }
                 // the block's other 64 channels are with the warp four on
@@ -463,8 +465,8 @@ cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uin
                      cudaStream_t stream)
 {
     auto *kernel = expert_gemm_kernel<OUT, TRANS, CLUSTER>;
-    cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)G_SMEM);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t st = allow_smem(reinterpret_cast<const void *>(kernel), (int)G_SMEM, allowed);
     if (st != cudaSuccess)
         return st;
     const int64_t wide = OUT == OUT_SWIGLU ? 2 * (int64_t)g.M : g.M;

@@ -308,8 +308,8 @@ template <int CLUSTER>
 cudaError_t run_wgrad(WgradArgs g, const void *dy, const void *x, cudaStream_t stream)
 {
     auto *kernel = expert_wgrad_kernel<CLUSTER>;
-    cudaError_t st = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)W_SMEM);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t st = allow_smem(reinterpret_cast<const void *>(kernel), (int)W_SMEM, allowed);
     if (st != cudaSuccess)
         return st;
     CUtensorMap map_dy, map_x;

@@ -2,6 +2,7 @@
 // validated by the caller; each returns the CUDA status of its launches.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -164,6 +165,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 {
     return launch_pdl_clusters(kernel, 1, grid, block, smem, stream, args...);
 }
+
+// Allows `kernel` its dynamic shared memory on the current device, once a device.
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &allowed);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

@@ -288,7 +288,7 @@ struct Work {
 };
 
 template <bool DOWN>
-__device__ Work few_work(const FewShared &s, const FewArgs &g)
+__device__ Work few_work(const FewShared &s, const FewArgs &g, int tile_bytes, int stages)
 {
     Work w = {};
     const int grid = gridDim.x, b = blockIdx.x;
@@ -300,18 +300,27 @@ __device__ Work few_work(const FewShared &s, const FewArgs &g)
         return w;
     }
     // tiles a CTA takes, and shares of the experts: the fewest bytes for the busiest
-    // CTA; of equals the most tiles, whose stages are the largest
+    // CTA, what a stage takes besides (some 0.1 us) and a join of the shares (1.5 us)
+    // counted as bytes too
+    constexpr int64_t STAGE = 4096, JOIN = 65536;
     const int all = (g.H + 15) / 16, experts = max(s.active, 1);
-    int best = 0, shares = 1, cost = 0x7fffffff;
+    int best = 0, shares = 1;
+    int64_t cost = INT64_MAX;
     for (int n = 1; n <= FEW_TILES; n++) {
         const int groups = (all + n - 1) / n;
-        const int sh = max(min(min(grid / groups, experts), FEW_MAX_SPLIT), 1);
-        const int rounds = (groups * sh + grid - 1) / grid;
-        const int c = rounds * n * ((experts + sh - 1) / sh);
-        if (c <= cost) {
-            cost = c;
-            best = n;
-            shares = sh;
+        for (int sh = 1; sh <= FEW_MAX_SPLIT; sh++) {
+            if (sh > 1 && (sh > experts || groups * sh > grid))
+                break;
+            const int rounds = (groups * sh + grid - 1) / grid;
+            const int64_t c =
+                (int64_t)rounds * ((experts + sh - 1) / sh) *
+                                  (n * tile_bytes + stages * STAGE) +
+                              (sh > 1) * JOIN;
+            if (c <= cost) {
+                cost = c;
+                best = n;
+                shares = sh;
+            }
         }
     }
     w.per = best;
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // warp % per, of slice warp / per; a pair of slices, a team, takes the two blocks
     // of every stage in its own slots of the ring.  (Who waits on a slot's barriers
     // does so in each of its phases: parity cannot tell a phase from the next but one.)
-    const Work whole = few_work<DOWN>(sh, g);
+    const Work whole = few_work<DOWN>(sh, g, 16 * K * (int)sizeof(W), (blocks + 1) / 2);
     const int per = DOWN ? whole.per : FEW_TILES;
     int teams = FEW_WARPS / per / 2;  // pairs of slices
     const int act_block = ((sh.longest + 7) & ~7) * PITCH;
@@ -842,8 +851,9 @@ template <typename W, int NG, bool DOWN>
 cudaError_t few(const FewMaps &maps, const FewArgs &g, cudaStream_t stream)
 {
     auto *kernel = few_kernel<W, NG, DOWN>;
-    const cudaError_t st = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t st =
+        allow_smem(reinterpret_cast<const void *>(kernel), (int)FEW_SMEM, allowed);
     if (st != cudaSuccess)
         return st;
     return launch_pdl(kernel, dim3(sm_count()), dim3(FEW_THREADS), FEW_SMEM, stream, maps, g);

@@ -60,18 +60,13 @@ __device__ inline void load_segments(Segments &s, const int32_t *offsets, int E,
     __syncthreads();
 }
 
-// The expert whose units hold number m (m < s.first[E]).
-__device__ __forceinline__ int expert_of_unit(const Segments &s, int E, int m)
+// The expert whose units hold number m (m < s.first[E]), looked for from expert `from`
+// on: the units that a CTA takes one after another are of the same or the next experts.
+__device__ __forceinline__ int expert_of_unit(const Segments &s, int m, int from)
 {
-    int lo = 0, hi = E;  // first[lo] <= m < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.first[mid] <= m)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
+    while (s.first[from + 1] <= m)
+        from++;
+    return from;
 }
 
 // 64 bytes of each of a warp's rows, a row's with its lane, to global memory: rows side
@@ -96,6 +91,22 @@ __device__ __forceinline__ void store_rows(uint8_t *way, const uint32_t (&v)[16]
         if (r < rows && piece * 16 < bytes)
             st_v4(to + r * stride + piece * 16, u);
     }
+}
+
+// v / (1 + exp(-v)) within 2^-21: exp(-v) = 2^t with t = -v log2(e) in two terms, the
+// first by the hardware's 2^x (2^-22), the second, at most 2^-17, to first order.  expf
+// and a correctly rounded division are 50 instructions a value: unrolled over an
+// epilogue's values more than a short launch can afford to fetch.
+__device__ __forceinline__ float silu(float v)
+{
+    const float log2e = 1.44269504f, log2e_rest = 1.92596303e-8f, ln2 = 0.693147181f;
+    const float t = -v * log2e;
+    const float rest = fmaf(-v, log2e, -t) - v * log2e_rest;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    if (fabsf(t) < 128.0f)  // beyond, e is 0 or infinite, and rest may be NaN
+        e = fmaf(e, rest * ln2, e);
+    return __fdividef(v, 1.0f + e);
 }
 
 // Scale and reciprocal of a block whose largest magnitude is amax, each one
