@@ -1,6 +1,7 @@
 /*
  * moe_ep.h -- C ABI of the GB300 MoE expert-parallel layout / dispatch / combine
- * library (libmoe_ep.so, sm_103a kernels).
+ * library (libmoe_ep.so, sm_103a kernels), with the router and the experts'
+ * products around them.
  *
  * Problem statement (shared by the pages): T tokens with hidden size H, each
  * routed by a top-k router to k of E experts; the experts are spread over R
@@ -671,9 +672,11 @@ MOE_API moe_status moe_expert_wgrad(int N, int M, int K, int E, const void *dy, 
  *   workspace moe_layer_few_workspace_bytes(T, k, H, I) bytes, 16-byte aligned;
  *             needs no initialisation, holds nothing between calls
  *
- * Activations stay bf16 (x) and, between the products, two bf16 terms of the
- * fp32 value; sums are fp32 in an order that depends on the arguments' sizes and the
- * routing alone.  T <= MOE_FEW_MAX_TOKENS, T*k <= MOE_FEW_MAX_PAIRS, k <= MOE_MAX_TOPK
+ * Between the products h is fp32.  The tensor core takes x as it is and h as two
+ * bf16 terms where the weights are bf16; with E4M3 weights, which widen to fp16, x as
+ * one fp16 term and h as two, scaled by a power of two for each token and 128 inputs
+ * (exact but for what lies 2^39 below the largest of those).  Sums are fp32, in an
+ * order that depends on the arguments' sizes and the routing alone.  T <= MOE_FEW_MAX_TOKENS, T*k <= MOE_FEW_MAX_PAIRS, k <= MOE_MAX_TOPK
  * (more: MOE_ERR_UNSUPPORTED); H and I multiples of 8, of 128 for E4M3.  A token
  * may name an expert twice.  Ids outside [0, E) set MOE_ERRBIT_BAD_INDEX and add
  * nothing.
