@@ -18,9 +18,20 @@
 //   warp 8      tensor copies, one of a block of the rows (a box of 128, 64 or 32) and
 //               one of the weights (2 x 128 outputs): issuing one takes some 100 cycles
 //   warps 9,10  issue the MMAs, blocks in turn, each into its half of tensor memory (a
-//               block's waits, MMAs and commits take a warp longer than the MMAs)
+//               block's waits, MMAs and commits take a warp longer than the MMAs).
+//               Issued by the promotion warps themselves, with a half for each warpgroup,
+//               the same work took 1.4 times as long
 // For SwiGLU the two 128-output halves are gate and up of the same 128
 // channels, which makes a row's quantisation block the tile's own.
+// In clusters of two, for experts of many rows, the CTAs do neighbouring row
+// tiles of the same columns and each brings one half of the weights to both.
+//
+// What bounds it.  Few rows an expert: the weights' bytes (2048 rows over 64 experts,
+// K = 2048, M = 7168: 0.97 GB in 153 us, 0.94 of the copy rate).  Many: neither the
+// tensor pipe, busy for 56 % of the cycles on 16384 rows over 16 experts, nor the HBM, but
+// the turns of tensor memory between MMAs and promotion (two blocks' sums fill it), and
+// the L2, which delivers 12.8 TB/s.  65536 rows: K = 7168, 2 x 2048 outputs with SwiGLU
+// over 128 experts 1.93 ms (2.0 PFLOP/s), K = 2048, M = 7168 over 256 experts 1.23 ms.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -353,7 +364,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     warp_wait(ok, smem_addr(&sh.sums_full[d]), d_phase);
                     if (busy) {
                         tcgen05_after_sync();
-                        // the next 32 sums are on their way while these are added
+                        // 64 sums at a time, registers hold no more beside the running ones;
+                        // meanwhile the other warp of this quarter adds
                         const uint32_t from = mine + d * G_COLS;
                         uint32_t p[2][32];
                         tmem_ld32(from, p[0]);
@@ -362,11 +374,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
                             if (q == 2) {
- tmem_ld32(from + 128, p[0]);
- tmem_ld32(from + 160, p[1]);
- tmem_wait_ld();
-}
-                            if (q == 2) {
+                                tmem_ld32(from + 128, p[0]);
+                                tmem_ld32(from + 160, p[1]);
+                                tmem_wait_ld();
                                 tcgen05_before_sync();
                                 warp_arrive(smem_addr(&sh.sums_empty[d]));
                             }
@@ -511,9 +521,11 @@ template <int OUT, bool TRANS>
 cudaError_t run_gemm(const GemmArgs &g, int64_t K, const uint8_t *a_q, const uint8_t *w_q,
                      cudaStream_t stream)
 {
-    // Pairs of row tiles share the weights' way through the L2 where experts have a
-    // tile's rows on average
-    if ((int64_t)g.N >= (int64_t)G_ROWS * g.E)
+    // Pairs of row tiles share the weights' way through the L2, but wait for each other,
+    // and the odd tile of an expert shares nothing.  K = 2048, M = 7168, apart and in
+    // pairs: 64 experts of 64 rows 157 and 161 us, of 128 rows 199 and 205, of 192 rows
+    // 263 and 261; 256 experts of 256 rows 1.35 and 1.23 ms
+    if ((int64_t)g.N >= (int64_t)192 * g.E)
         return run_gemm<OUT, TRANS, 2>(g, K, a_q, w_q, stream);
     return run_gemm<OUT, TRANS, 1>(g, K, a_q, w_q, stream);
 }

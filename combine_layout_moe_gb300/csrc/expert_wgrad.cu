@@ -13,6 +13,11 @@
 // The tensor core's fp32 sum truncates: 2.1e-6 relative after 2048 rows, growing
 // with their number.  Each 1024 rows it starts from zero, and the chunks are added
 // with rounding in registers.
+//
+// Bound by its copies: 2048 rows an expert, M = 4096, K = 7168, 16 experts take 1.50 ms
+// (1.28 PFLOP/s); with the wait for the copies taken out 1.06 ms (the tensor pipe's
+// rate), with the stores taken out 1.33 ms, without clusters 1.63 ms, and in clusters of
+// four (which 144 of the SMs can hold) 1.57 ms.
 #include "common.cuh"
 #include "launch.h"
 #include "segments.cuh"
