@@ -31,7 +31,7 @@
 //
 // One token through 8 of 256 E4M3 experts, H = 7168, I = 2048: 70 us for 352 MB, 0.74 of
 // the copy rate; the rest is the two kernels' starts, lists and drains.  61 tokens, top-8
-// of 128, H = 4096, I = 1408: 505 us for 2.17 GB, 0.63: with four to eleven tokens an
+// of 128, H = 4096, I = 1408: 446 us for 2.17 GB, 0.72: with four to eleven tokens an
 // expert a stage takes its slot of the ring longer (copies alone: 0.88).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -344,8 +344,8 @@ struct Pass {
 };
 
 struct Work {
-    // UP: [q, end) over (expert in use, group of 8 channels).  DOWN: [q, end) over
-    // the experts of this CTA's share; `tile`, `tiles` its rows
+    // UP: [q, end) over (expert in use, group of 8 channels), in `shares` rounds.
+    // DOWN: [q, end) over the experts of this CTA's share; `tile`, `tiles` its rows
     int64_t q, end;
     int per, tile, tiles, split, shares;
 };
@@ -354,12 +354,13 @@ template <bool DOWN>
 __device__ Work few_work(const FewShared &s, const FewArgs &g, int tile_bytes, int stages)
 {
     Work w = {};
-    const int grid = gridDim.x, b = blockIdx.x;
+    const int grid = gridDim.x;
     if (!DOWN) {
+        // pieces of a pass, one of each round to a CTA: experts of many tokens, whose
+        // stages take longer, come to all CTAs alike
         w.per = g.I / 8;
         const int64_t all = (int64_t)s.active * w.per;
-        w.q = all * b / grid;
-        w.end = all * (b + 1) / grid;
+        w.shares = max((int)((all + grid * FEW_TILES - 1) / (grid * FEW_TILES)), 1);
         return w;
     }
     // tiles a CTA takes, and shares of the experts: the fewest bytes for the busiest
@@ -389,6 +390,22 @@ __device__ Work few_work(const FewShared &s, const FewArgs &g, int tile_bytes, i
     w.per = best;
     w.shares = shares;
     return w;
+}
+
+// DOWN: the first expert of a share.  Shares are even in what an expert's stages take:
+// its bytes, counted as eight tokens, and its tokens.
+__device__ __forceinline__ int few_share(const FewShared &s, int split, int shares)
+{
+    const int all = 8 * s.active + s.row0[s.active];
+    int lo = 0, hi = s.active;
+    while (lo < hi) {  // the first whose middle is behind all * split / shares
+        const int a = (lo + hi) >> 1;
+        if ((8 * (2 * a + 1) + s.row0[a] + s.row0[a + 1]) * shares <= 2 * all * split)
+            lo = a + 1;
+        else
+            hi = a;
+    }
+    return lo;
 }
 
 template <bool DOWN>
@@ -572,7 +589,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
     const int row_tiles = (g.H + 15) / 16;
     const int groups = DOWN ? (row_tiles + whole.per - 1) / whole.per : 0;
-    const int jobs = DOWN ? groups * whole.shares : (int)gridDim.x;
+    const int jobs = DOWN ? groups * whole.shares : whole.shares * (int)gridDim.x;
     int s = 0, turn = 0;  // the slot, and the team whose it is
     uint32_t phase = 0, meetings = 0;
     uint32_t used = 0, parity = 0;  // a loader's slots that it filled, and their last phase
@@ -585,8 +602,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             work.split = job - group * whole.shares;
             work.tile = group * whole.per;
             work.tiles = min(whole.per, row_tiles - work.tile);
-            work.q = (int64_t)sh.active * work.split / whole.shares;
-            work.end = (int64_t)sh.active * (work.split + 1) / whole.shares;
+            work.q = few_share(sh, work.split, whole.shares);
+            work.end = few_share(sh, work.split + 1, whole.shares);
+        } else {
+            const int64_t all = (int64_t)sh.active * whole.per;
+            work.q = all * job / jobs;
+            work.end = all * (job + 1) / jobs;
         }
 
         if (warp >= FEW_WARPS) {  // loaders
