@@ -29,10 +29,11 @@
 // it adds up in shared memory; where experts are shared out, the last CTA of a group
 // of rows adds the shares in a fixed order.
 //
-// One token through 8 of 256 E4M3 experts, H = 7168, I = 2048: 70 us for 352 MB, 0.74 of
+// One token through 8 of 256 E4M3 experts, H = 7168, I = 2048: 69 us for 352 MB, 0.75 of
 // the copy rate; the rest is the two kernels' starts, lists and drains.  61 tokens, top-8
-// of 128, H = 4096, I = 1408: 446 us for 2.17 GB, 0.72: with four to eleven tokens an
-// expert a stage takes its slot of the ring longer (copies alone: 0.88).
+// of 128, H = 4096, I = 1408: 426 us for 2.17 GB, 0.75: UP 240 us for 1.44 GB, DOWN 195 us
+// for 0.72 GB, whose consumers (two groups of columns for five tokens, a pass of six
+// stages) fall behind the copies.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -48,11 +49,13 @@ namespace {
 constexpr int FEW_WARPS = 16;   // consumers
 constexpr int FEW_TILES = 8;    // most tiles of a stage
 constexpr int FEW_LOADERS = 4;
+constexpr int FEW_BATCH = 4;  // tokens that a loader has in flight
 constexpr int FEW_THREADS = 32 * (FEW_WARPS + FEW_LOADERS);
 constexpr int FEW_MAX_STAGES = 16;
 constexpr int FEW_ROWS = 32;      // most tokens of an entry
 constexpr int FEW_TILE = 2048;     // 16 rows x 128 bytes
-constexpr int FEW_FACTORS = 1024;  // of a stage: a power of two for each token and block
+constexpr int FEW_FACTORS = 512;  // of a stage: a power of two for each token and block, and
+                                  // the weights' scales of each tile and block
 constexpr int FEW_MAX_SPLIT = 8;   // CTAs that may share the experts of a row group
 constexpr size_t FEW_SMEM = 227 * 1024;
 
@@ -73,15 +76,19 @@ struct FewType<__nv_bfloat16> {
 
 struct FewShared {
     uint64_t full[FEW_MAX_STAGES], ready[FEW_MAX_STAGES], empty[FEW_MAX_STAGES];
-    uint64_t given[FEW_TILES], taken[FEW_TILES];  // UP: a tile's sums of the second slice
-    uint32_t tokens[2][MOE_MAX_EXPERTS];   // bit t: expert e is named by token t
-    int ids[MOE_FEW_MAX_PAIRS];            // topk_idx
+    uint64_t given[FEW_TILES], taken[FEW_TILES];  // of two slices that add up a tile's sums
     int act[MOE_FEW_MAX_PAIRS];            // entries: experts in use, by id
     int row0[MOE_FEW_MAX_PAIRS + 1];       // first row of each in h, at most 32 an entry
     float w[MOE_FEW_MAX_PAIRS];            // weight of each row
     uint8_t token[MOE_FEW_MAX_PAIRS];      // token of each row
-    int16_t pos[MOE_MAX_EXPERTS];          // first entry of e
     int active, longest, last;
+};
+
+// What few_lists works with, in the ring before it is one.
+struct FewScratch {
+    uint32_t tokens[2][MOE_MAX_EXPERTS];  // bit t: expert e is named by token t
+    int ids[MOE_FEW_MAX_PAIRS];           // topk_idx
+    int16_t pos[MOE_MAX_EXPERTS];         // first entry of e
 };
 
 // Weights in boxes of 1, 2, 4 and 8 tiles' rows and two blocks.  Five dimensions: 128
@@ -120,7 +127,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr)
     return v;
 }
 
-
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -136,7 +142,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 __device__ __forceinline__ void mma_16816(__nv_bfloat16, float (&c)[4], const uint32_t (&a)[4],
                                           uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -146,7 +152,7 @@ __device__ __forceinline__ void mma_16816(__nv_bfloat16, float (&c)[4], const ui
 __device__ __forceinline__ void mma_16816(__half, float (&c)[4], const uint32_t (&a)[4],
                                           uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -253,7 +259,8 @@ __device__ void few_lists_short(FewShared &s, const FewArgs &g, uint32_t *err_wo
 }
 
 // Who names whom, in shared memory; called by the whole CTA.
-__device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t *err_word)
+__device__ void few_lists(FewShared &s, FewScratch &l, const FewArgs &g, bool weights,
+                          uint32_t *err_word)
 {
     const int pairs = g.T * g.k;
     if (pairs <= 32) {
@@ -263,7 +270,7 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
         return;
     }
     for (int e = threadIdx.x; e < g.E; e += FEW_THREADS)
-        s.tokens[0][e] = s.tokens[1][e] = 0;
+        l.tokens[0][e] = l.tokens[1][e] = 0;
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += FEW_THREADS) {
         int e = g.idx[p];
@@ -272,9 +279,9 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
             e = -1;
         } else {
             const int t = p / g.k;
-            atomicOr(&s.tokens[t >> 5][e], 1u << (t & 31));
+            atomicOr(&l.tokens[t >> 5][e], 1u << (t & 31));
         }
-        s.ids[p] = e;
+        l.ids[p] = e;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -282,7 +289,7 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
         int n = 0, rows = 0, longest = 0;
         for (int e0 = 0; e0 < g.E; e0 += 32) {
             const int e = e0 + lane;
-            const int mine = e < g.E ? __popc(s.tokens[0][e]) + __popc(s.tokens[1][e]) : 0;
+            const int mine = e < g.E ? __popc(l.tokens[0][e]) + __popc(l.tokens[1][e]) : 0;
             if (!__any_sync(FULL_MASK, mine > 0))
                 continue;
             const int entries = (mine + FEW_ROWS - 1) / FEW_ROWS;
@@ -299,7 +306,7 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
                 s.row0[at + i] = row + i * FEW_ROWS;
             }
             if (entries > 0)
-                s.pos[e] = (int16_t)at;
+                l.pos[e] = (int16_t)at;
             const int all = __shfl_sync(FULL_MASK, sum, 31);
             n += all >> 16;
             rows += all & 0xffff;
@@ -314,23 +321,23 @@ __device__ void few_lists(FewShared &s, const FewArgs &g, bool weights, uint32_t
     }
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += FEW_THREADS) {
-        const int e = s.ids[p], t = p / g.k, first = t * g.k;
+        const int e = l.ids[p], t = p / g.k, first = t * g.k;
         if (e < 0)
             continue;
         bool again = false;  // an earlier slot of the token names the same expert
         for (int q = first; q < p; q++)
-            again |= s.ids[q] == e;
+            again |= l.ids[q] == e;
         if (again)
             continue;
-        const uint32_t lo = s.tokens[0][e], hi = s.tokens[1][e];
+        const uint32_t lo = l.tokens[0][e], hi = l.tokens[1][e];
         const int below = t < 32 ? __popc(lo & ((1u << t) - 1))
                                  : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1));
-        const int row = s.row0[s.pos[e]] + below;
+        const int row = s.row0[l.pos[e]] + below;
         s.token[row] = (uint8_t)t;
         if (weights) {
             float w = 0.0f;
             for (int q = p; q < first + g.k; q++)
-                if (s.ids[q] == e)
+                if (l.ids[q] == e)
                     w += g.topk_w[q];
             s.w[row] = w;
         }
@@ -528,16 +535,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // bytes of a row of activations in a block, padded so that the rows of a group
     // start in different banks: 4 inputs of both terms are 16 bytes, of one term 8
     constexpr int PITCH = DOWN ? TY::KB * 4 + 64 : TY::KB * 2 + 32;
-    constexpr int GIVEN = 128 * NG;                  // sums of a tile
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                 ~(uintptr_t)1023);
-    uint8_t *top = raw + FEW_SMEM;
-    FewShared &sh = *reinterpret_cast<FewShared *>(top - sizeof(FewShared));
-    // UP: for each tile the second slice's sums, on their way to the first; DOWN: for
-    // each warp the sums of 16 outputs x T tokens
-    float *sums = reinterpret_cast<float *>(top - sizeof(FewShared)) -
-                  (DOWN ? FEW_WARPS * 16 * g.T : FEW_TILES * GIVEN);
+    FewShared &sh = *reinterpret_cast<FewShared *>(raw + FEW_SMEM - sizeof(FewShared));
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int K = DOWN ? g.I : g.H;
     const int blocks = (K + TY::KB - 1) / TY::KB;
@@ -552,25 +553,36 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (i < g.groups)
             g.arrived[i] = 0;
     }
-    few_lists(sh, g, !DOWN, !DOWN && blockIdx.x == 0 ? g.err_word : nullptr);
+    few_lists(sh, *reinterpret_cast<FewScratch *>(ring), g, !DOWN,
+              !DOWN && blockIdx.x == 0 ? g.err_word : nullptr);
 
     // Stage: two blocks of inputs of up to `per` tiles, and of the activations of as
-    // many tokens as the largest entry has, in groups of eight.  Warp: tile
+    // many tokens as the largest entry has.  Warp: tile
     // warp % per, of slice warp / per; a pair of slices, a team, takes the two blocks
     // of every stage in its own slots of the ring.  (Who waits on a slot's barriers
     // does so in each of its phases: parity cannot tell a phase from the next but one.)
     const Work whole = few_work<DOWN>(sh, g, 16 * K * (int)sizeof(W), (blocks + 1) / 2);
     const int per = DOWN ? whole.per : FEW_TILES;
     int teams = FEW_WARPS / per / 2;  // pairs of slices
-    const int act_block = ((sh.longest + 7) & ~7) * PITCH;
+    // (the mma's columns behind the last token read whatever comes there in shared memory)
+    const int act_block = sh.longest * PITCH;
     const int w_bytes = 2 * per * FEW_TILE;
     const int act_at = w_bytes + (FP8 ? FEW_FACTORS : 0);
     const int stage_bytes = (act_at + 2 * act_block + 1023) & ~1023;
-    // at least two: a stage is 70 KB at most, and the ring has 140
+    // UP: for each tile the second slice's sums, on their way to the first; DOWN: for each
+    // tile and team the sums of 16 outputs x T tokens
+    const int given = 128 * ((sh.longest + 7) >> 3);
+    float *sums = reinterpret_cast<float *>(&sh) - FEW_TILES * (DOWN ? 16 * g.T : given);
+    // at least two: a stage is 70 KB at most, and the ring has 180
     int stages = min((int)(reinterpret_cast<uint8_t *>(sums) - ring) / stage_bytes,
                      FEW_MAX_STAGES);
     teams = min(teams, stages);
     stages -= stages % teams;
+    // Tokens for more than a batch take a loader longer than the copies: then all have as
+    // many slots (9 tokens, five slots of four loaders: 254 us for UP instead of 240;
+    // one token, four slots instead of five: 71.4 us for the layer instead of 69.7)
+    if (sh.longest > FEW_BATCH && stages > FEW_LOADERS && FEW_LOADERS % teams == 0)
+        stages -= stages % FEW_LOADERS;
     const int slices = 2 * teams;
     const bool pairs = K % TY::KB == 0;  // how the maps are made
     if (threadIdx.x == 0) {
@@ -584,6 +596,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             mbar_init(smem_addr(&sh.taken[i]), 1);
         }
         mbar_fence_init();
+        fence_proxy_async_smem();  // the lists' scratch becomes the ring
     }
     __syncthreads();
 
@@ -613,7 +626,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (warp >= FEW_WARPS) {  // loaders
             constexpr int EACH = 2 * TY::KB / 32;  // inputs a lane brings of each token
             constexpr int WORDS = DOWN ? EACH : EACH / 2;
-            constexpr int BATCH = 4;               // tokens in flight
             const int block = lane >> 4, in_block = (lane & 15) * EACH;
             while (work.q < work.end) {
                 const Pass p = next_pass<DOWN>(work);
@@ -622,17 +634,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 for (int b = 0; b < blocks; b += 2) {
                     if (s % FEW_LOADERS == warp - FEW_WARPS) {
                         const int k = (b + block) * TY::KB + in_block;
-                        uint32_t raws[BATCH][WORDS];
-                        auto load = [&](int j0) {
-#pragma unroll
-                            for (int j = 0; j < BATCH; j++) {
-                                const int row = row0 + min(j0 + j, n - 1);
-                                few_load<DOWN, EACH>(raws[j], g, DOWN ? row : sh.token[row], k,
-                                                     K);
-                            }
+                        uint32_t raws[FEW_BATCH][WORDS];
+                        auto load_one = [&](int j, int token) {
+                            const int row = row0 + token;
+                            few_load<DOWN, EACH>(raws[j], g, DOWN ? row : sh.token[row], k, K);
                         };
+                        auto load = [&] {
+#pragma unroll
+                            for (int j = 0; j < FEW_BATCH; j++)
+                                if (j < n)
+                                    load_one(j, j);
+                        };
+                        float scale = 0.0f;
+                        if (FP8) {  // of a block, tile and (UP) gate or up
+                            const int tile = p.tile + min(lane & 7, p.tiles - 1);
+                            const int at = min(b + block, blocks - 1);
+                            const int row = DOWN ? e * (g.H / 128) + tile / 8
+                                                 : e * (2 * g.I / 128) + tile / 16 +
+                                                       (lane >> 3 & 1) * (g.I / 128);
+                            scale = g.scales[(int64_t)row * blocks + at];
+                        }
                         if (!DOWN || used != 0)
-                            load(0);  // in flight during the wait
+                            load();  // in flight during the wait
                         warp_wait(ok, smem_addr(&sh.empty[s]), phase ^ 1);
                         const uint32_t bar = smem_addr(&sh.full[s]);
                         uint8_t *stage = ring + s * stage_bytes;
@@ -658,18 +681,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                         __syncwarp();
                         if (DOWN && used == 0) {
                             wait_prior_grid();
-                            load(0);
+                            load();
                         }
                         used |= (uint32_t)ok << s;
                         parity = (parity & ~(1u << s)) | phase << s;
                         float *factors =
                             reinterpret_cast<float *>(stage + w_bytes) + block * FEW_ROWS;
                         const uint32_t act = smem_addr(stage) + act_at + block * act_block;
-                        for (int j0 = 0; j0 < n; j0 += BATCH) {
-                            if (j0 > 0)
-                                load(j0);
+                        if (FP8)  // behind the powers of two
+                            reinterpret_cast<float *>(stage + w_bytes)[2 * FEW_ROWS + lane] =
+                                scale;
+                        for (int j0 = 0; j0 < n; j0 += FEW_BATCH) {
 #pragma unroll
-                            for (int j = 0; j < BATCH; j++) {
+                            for (int j = 0; j < FEW_BATCH; j++) {
                                 if (j0 + j >= n)
                                     break;
                                 float f = 1.0f;
@@ -689,6 +713,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                                         v[2 * i + 1] = bf16hi(raws[j][i]) * f;
                                     }
                                 }
+                                if (j0 + j + FEW_BATCH < n)  // the next in its place
+                                    load_one(j, j0 + j + FEW_BATCH);
                                 few_store<Act, DOWN, EACH>(act + (j0 + j) * PITCH, in_block, v);
                             }
                         }
@@ -706,16 +732,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (DOWN) {
             wait_prior_grid();
             named_barrier(1, 32 * FEW_WARPS);  // the job before has been read
-            for (int i = lane; i < 16 * g.T; i += 32)
-                sums[warp * 16 * g.T + i] = 0.0f;
-            __syncwarp();
         }
         const int r8 = lane >> 2, c4 = lane & 3;  // this lane's row (and row + 8) and columns
         const int slice = warp / per, in_pass = warp - slice * per;
         const bool member = slice < slices;
+        const int plane = (slice >> 1) * per + in_pass;  // its team's sums of the tile
+        if (DOWN && member && !(slice & 1))  // the first to add
+            for (int i = lane; i < 16 * g.T; i += 32)
+                sums[plane * 16 * g.T + i] = 0.0f;
+        __syncwarp();
         while (work.q < work.end) {
             const Pass p = next_pass<DOWN>(work);
-            const int e = sh.act[p.a], row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
+            const int row0 = sh.row0[p.a], n = sh.row0[p.a + 1] - row0;
             const bool busy = member && in_pass < p.tiles;
             const int tile = p.tile + in_pass;
             // where the tile lies in a block, and how far a block's next tile's rows,
@@ -732,72 +760,66 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             const uint32_t act_offset =
                 act_at + (slice & 1) * act_block +
                 (DOWN ? (r8 >> 1) * PITCH + c4 * 16 + (r8 & 1) * 8 : r8 * PITCH + c4 * 8);
-            const float *s_lo = nullptr, *s_hi = nullptr;  // of rows 0-7 and 8-15
-            float v_lo = 0.0f, v_hi = 0.0f;
-            if (FP8 && busy) {
-                if (DOWN) {
-                    s_lo = g.scales + ((int64_t)e * (g.H / 128) + tile / 8) * blocks;
-                    s_hi = s_lo;
-                } else {
-                    s_lo = g.scales + ((int64_t)e * (2 * g.I / 128) + tile / 16) * blocks;
-                    s_hi = s_lo + (int64_t)(g.I / 128) * blocks;
-                }
-            }
             float acc[GROUPS][SUMS];
 #pragma unroll
             for (int i = 0; i < GROUPS; i++)
 #pragma unroll
                 for (int c = 0; c < SUMS; c++)
                     acc[i][c] = 0.0f;
-            for (int b0 = 0, mine = 0; b0 < blocks; b0 += 2) {
+            for (int b0 = 0; b0 < blocks; b0 += 2) {
                 const bool take = member && turn == slice >> 1;
                 if (++turn == teams)
                     turn = 0;
                 const int b = b0 + (slice & 1);
                 if (take) {
-                    if (FP8 && busy && (mine & 31) == 0) {  // of the next 32 blocks, one a lane
-                        const int at = min(b + lane * slices, blocks - 1);
-                        v_lo = s_lo[at];
-                        v_hi = s_hi[at];
-                    }
                     warp_wait2(ok, smem_addr(&sh.ready[s]), phase, smem_addr(&sh.full[s]), phase);
                 }
                 if (take && busy && b < blocks) {
                     const uint8_t *stage = ring + s * stage_bytes;
                     const uint32_t wt = smem_addr(stage) + tile_at;
+                    const uint32_t act = smem_addr(stage) + act_offset;
+                    // everything out of shared memory before the first result is used
+                    uint32_t w[4][4];  // rows 0-7 and 8-15 of 16-byte pieces 2j and 2j + 1
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        ldsm4(wt + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4), w[j]);
+                    uint2 v[TY::STEPS];  // a group's activations
+#pragma unroll
+                    for (int j = 0; j < TY::STEPS; j++)
+                        v[j] = lds64(act + j * (DOWN ? 64 : 32));
                     uint32_t a[TY::STEPS][4];
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        uint32_t v[4];  // rows 0-7 and 8-15 of 16-byte pieces 2j and 2j + 1
-                        ldsm4(wt + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4), v);
                         if constexpr (FP8) {
-                            widen(v[0], a[2 * j][0], a[2 * j][2]);
-                            widen(v[1], a[2 * j][1], a[2 * j][3]);
-                            widen(v[2], a[2 * j + 1][0], a[2 * j + 1][2]);
-                            widen(v[3], a[2 * j + 1][1], a[2 * j + 1][3]);
+                            widen(w[j][0], a[2 * j][0], a[2 * j][2]);
+                            widen(w[j][1], a[2 * j][1], a[2 * j][3]);
+                            widen(w[j][2], a[2 * j + 1][0], a[2 * j + 1][2]);
+                            widen(w[j][3], a[2 * j + 1][1], a[2 * j + 1][3]);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; i++)
-                                a[j][i] = v[i];
+                                a[j][i] = w[j][i];
                         }
                     }
-                    float f_lo = 1.0f, f_hi = 1.0f;
+                    float f_lo = 1.0f, f_hi = 1.0f;  // of rows 0-7 and 8-15
                     if (FP8) {
-                        f_lo = __shfl_sync(FULL_MASK, v_lo, mine & 31);
-                        f_hi = __shfl_sync(FULL_MASK, v_hi, mine & 31);
+                        const float *scales = reinterpret_cast<const float *>(stage + w_bytes) +
+                                              2 * FEW_ROWS + (slice & 1) * 16 + in_pass;
+                        f_lo = scales[0];
+                        f_hi = DOWN ? f_lo : scales[8];
                     }
-                    mine++;
-                    const uint32_t act = smem_addr(stage) + act_offset;
 #pragma unroll
                     for (int grp = 0; grp < GROUPS; grp++) {
                         if (grp * GROUP < n) {
                             float part[2][4] = {};  // sums that do not wait for each other
-                            const uint32_t row = act + grp * GROUP * PITCH;
+                            if (grp > 0) {
 #pragma unroll
-                            for (int j = 0; j < TY::STEPS; j++) {
-                                const uint2 v = lds64(row + j * (DOWN ? 64 : 32));
-                                mma_16816(Act(), part[j & 1], a[j], v.x, v.y);
+                                for (int j = 0; j < TY::STEPS; j++)
+                                    v[j] = lds64(act + grp * GROUP * PITCH + j * (DOWN ? 64 : 32));
                             }
+#pragma unroll
+                            for (int j = 0; j < TY::STEPS; j++)
+                                mma_16816(Act(), part[j & 1], a[j], v[j].x, v[j].y);
                             // the columns' powers of two
                             const float *back = reinterpret_cast<const float *>(stage + w_bytes) +
                                                 (slice & 1) * FEW_ROWS + grp * GROUP;
@@ -834,32 +856,40 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             if (!busy)
                 continue;
             if constexpr (!DOWN) {  // the two slices' sums meet
-                float *x = sums + in_pass * GIVEN + lane;
+                float *x = sums + in_pass * given + lane;
                 const uint32_t now = meetings++ & 1;
                 if (slice == 1) {
                     warp_wait(ok, smem_addr(&sh.taken[in_pass]), now ^ 1);
 #pragma unroll
                     for (int i = 0; i < 4 * NG; i++)
-                        x[i * 32] = acc[i / 4][i % 4];
+                        if (i / 4 * 8 < n)
+                            x[i * 32] = acc[i / 4][i % 4];
                     warp_arrive(smem_addr(&sh.given[in_pass]));
                     continue;
                 }
                 warp_wait(ok, smem_addr(&sh.given[in_pass]), now);
 #pragma unroll
                 for (int i = 0; i < 4 * NG; i++)
-                    acc[i / 4][i % 4] += x[i * 32];
+                    if (i / 4 * 8 < n)
+                        acc[i / 4][i % 4] += x[i * 32];
                 warp_arrive(smem_addr(&sh.taken[in_pass]));
             }
-            if constexpr (DOWN) {
+            if constexpr (DOWN) {  // a team's two slices add in turn, the first before the second
+                const uint32_t now = meetings++ & 1;
+                if (slice & 1)
+                    warp_wait(ok, smem_addr(&sh.given[plane]), now);
+                else
+                    warp_wait(ok, smem_addr(&sh.taken[plane]), now ^ 1);
 #pragma unroll
                 for (int grp = 0; grp < GROUPS; grp++) {
                     const int col = grp * GROUP + c4;
                     if (col < n) {
-                        float *to = sums + (warp * g.T + sh.token[row0 + col]) * 16 + r8;
+                        float *to = sums + (plane * g.T + sh.token[row0 + col]) * 16 + r8;
                         to[0] += acc[grp][0];
                         to[8] += acc[grp][1];
                     }
                 }
+                warp_arrive(smem_addr(slice & 1 ? &sh.taken[plane] : &sh.given[plane]));
             } else {
 #pragma unroll
                 for (int grp = 0; grp < GROUPS; grp++) {
@@ -879,13 +909,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
         if (DOWN) {
             named_barrier(1, 32 * FEW_WARPS);  // every warp's sums are complete
-            // the slices of a tile, added up by its first warp
+            // the teams of a tile, added up by its first warp
             const int o = (work.tile + warp) * 16 + (lane & 15);
             const bool mine = warp < work.tiles && o < g.H;
             float *tile_sums = sums + warp * 16 * g.T + (lane & 15);
             if (mine)
                 for (int t = lane >> 4; t < g.T; t += 2)
-                    for (int i = 1; i < slices; i++)
+                    for (int i = 1; i < teams; i++)
                         tile_sums[t * 16] += tile_sums[(i * per * g.T + t) * 16];
             if (whole.shares > 1) {
                 const int64_t plane = (int64_t)g.T * g.H;
