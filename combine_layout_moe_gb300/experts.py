@@ -8,7 +8,7 @@ dispatch and combine.
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+from typing import Dict, NamedTuple, Optional
 
 import torch
 
@@ -208,8 +208,10 @@ def moe_layer_few(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     else:
         _want(out, "out", out_dtype, (T, H))
     if workspace is None:
-        workspace = torch.empty(moe_layer_few_workspace_bytes(T, k, H, inner), dtype=torch.uint8,
-                                device=x.device)
+        # of the stream's own memory: it is free for others when the call returns
+        with torch.cuda.stream(stream):  # None: the current one
+            workspace = torch.empty(moe_layer_few_workspace_bytes(T, k, H, inner),
+                                    dtype=torch.uint8, device=x.device)
     _check(_lib.moe_layer_few(T, k, H, inner, E, _ptr(x), _ptr(topk_idx), _ptr(topk_w),
                               _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
                               MOE_W_E4M3 if fp8 else MOE_W_BF16, _ptr(out), code,
@@ -224,7 +226,8 @@ class MoELayer:
 
     Holds the experts' E4M3 weights and scales (w13 [E, 2I, H], w2 [E, H, I],
     gate rows of w13 first).  Calling it with x [T, H] bf16 and the router's
-    logits [T, E] returns [T, H]; device-side errors collect in `err_word`.
+    logits [T, E] returns [T, H]; device-side errors collect in `err_word`.  Calls on
+    several streams keep a layout workspace each.
     """
 
     def __init__(self, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
@@ -234,7 +237,7 @@ class MoELayer:
         self.w13, self.w13_scales, self.w2, self.w2_scales = w13, w13_scales, w2, w2_scales
         self.k, self.groups, self.topk_groups = k, groups, topk_groups
         self.err_word = new_error_word(w13.device)
-        self._layout_ws: Optional[torch.Tensor] = None
+        self._layout_ws: Dict[int, torch.Tensor] = {}  # of each stream
 
     def few(self, T: int) -> bool:
         """Whether a batch of T tokens takes the two-kernel form."""
@@ -243,21 +246,23 @@ class MoELayer:
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, *,
                  out_dtype: torch.dtype = torch.bfloat16,
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        if stream is not None:
+            # what is made on the way comes from that stream's memory, and so does the result
+            with torch.cuda.stream(stream):
+                return self(x, logits, out_dtype=out_dtype)
         T, E = logits.shape
         err = self.err_word
-        idx, w = moe_route(logits, self.k, groups=self.groups, topk_groups=self.topk_groups,
-                           stream=stream)
+        idx, w = moe_route(logits, self.k, groups=self.groups, topk_groups=self.topk_groups)
         if self.few(T):
             return moe_layer_few(x, idx, w, self.w13, self.w2, w13_scales=self.w13_scales,
-                                 w2_scales=self.w2_scales, out_dtype=out_dtype, err_word=err,
-                                 stream=stream)
+                                 w2_scales=self.w2_scales, out_dtype=out_dtype, err_word=err)
         need = moe_layout_workspace_bytes(T, self.k, E)
-        if self._layout_ws is None or self._layout_ws.numel() < need:
-            self._layout_ws = new_workspace(need, x.device)
-        lay, q, s = moe_layout_dispatch_quant(x, idx, E, 1, workspace=self._layout_ws,
-                                              err_word=err, stream=stream)
+        key = torch.cuda.current_stream(x.device).cuda_stream
+        ws = self._layout_ws.get(key)
+        if ws is None or ws.numel() < need:
+            ws = self._layout_ws[key] = new_workspace(need, x.device)
+        lay, q, s = moe_layout_dispatch_quant(x, idx, E, 1, workspace=ws, err_word=err)
         h, hs = moe_expert_swiglu(q, s, lay.expert_offsets, self.w13, self.w13_scales,
-                                  err_word=err, stream=stream)
-        y = moe_expert_gemm(h, hs, lay.expert_offsets, self.w2, self.w2_scales, err_word=err,
-                            stream=stream)
-        return moe_combine(y, lay.slot_of, w, out_dtype=out_dtype, err_word=err, stream=stream)
+                                  err_word=err)
+        y = moe_expert_gemm(h, hs, lay.expert_offsets, self.w2, self.w2_scales, err_word=err)
+        return moe_combine(y, lay.slot_of, w, out_dtype=out_dtype, err_word=err)

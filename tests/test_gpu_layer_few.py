@@ -175,3 +175,34 @@ def test_layer_takes_both_forms():
     ref, _ = reference(x, idx, w, w13, s13, w2, s2)
     assert (short.double() - ref).norm() / ref.norm() < 0.003   # bf16 output
     assert (long.double() - ref).norm() / ref.norm() < 0.06     # E4M3 rows before each product
+
+
+@pytest.mark.parametrize("T,few", [(16, True), (16, False), (100, False)])
+def test_on_another_stream(T, few):
+    """Memory of the calling stream, given out again while another stream has the call's
+    work still before it, is not part of that work."""
+    H, inner, E, k = 512, 256, 16, 4
+    p = m()
+    x, idx, w, w13, s13, w2, s2 = make(T, k, H, inner, E, True, seed=21)
+    logits = torch.randn((T, E), generator=gen(22), device="cuda")
+    layer = p.MoELayer(w13, s13, w2, s2, k)
+
+    def call(stream=None):
+        if few:
+            return p.moe_layer_few(x, idx, w, w13, w2, w13_scales=s13, w2_scales=s2,
+                                   stream=stream)
+        return layer(x, logits, stream=stream)
+
+    want = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = call(side)
+    sizes = [1 << i for i in range(9, 24)]
+    over = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in (0, 1)]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert len(over) == 2 * len(sizes)
+    assert torch.equal(got, want)
+    assert p.moe_read_error(layer.err_word) == 0
